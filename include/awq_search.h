@@ -81,7 +81,8 @@ typedef enum awq_status {
   AWQ_ERR_UNSUPPORTED_DEVICE = 7  /* the current device is not sm_100 */
 } awq_status;
 
-enum { AWQ_DTYPE_BF16 = 0, AWQ_DTYPE_F32 = 1 };
+/* AWQ_DTYPE_F16 and AWQ_DTYPE_E4M3 are types of the decode-step operators only. */
+enum { AWQ_DTYPE_BF16 = 0, AWQ_DTYPE_F32 = 1, AWQ_DTYPE_F16 = 2, AWQ_DTYPE_E4M3 = 3 };
 
 /* The candidates' quantizer. AWQ_QUANT_ASYM is the search's asymmetric zero-point
  * quantizer (AWQ-P1 §7, steps 3-4 below). AWQ_QUANT_SYM is the symmetric [-7, 7] absmax
@@ -354,6 +355,109 @@ int awq_w4a16_matmul_packed(const void* A, const int32_t* packed, const void* st
 /* The dequantized operand alone: out_wt [N][K] fp16 (K contiguous) = w16 transposed. */
 int awq_w4a16_dequant(const int32_t* codes, const void* steps, const void* zeros,
                       int64_t K, int64_t N, int group, void* out_wt, awq_stream_t stream);
+
+/* ---- The other operators of a decode step -------------------------------------------
+ * Around the W4A16 products of a quantized attention block: the norm that produces the
+ * activations, the append of the new keys and values to a paged cache with the position
+ * rotation on the way, and the attention of the new tokens over that cache:
+ *   awq_rms_norm -> awq_w4a16_matmul_packed (QKV) -> awq_kv_append -> awq_paged_attention
+ *   -> awq_w4a16_matmul_packed (output projection) -> awq_rms_norm -> ...
+ * All are asynchronous on `stream` (launch errors are reported), allocate nothing, keep
+ * nothing between calls and give equal bits for equal inputs; calls from several host
+ * threads and streams may overlap if their outputs and work spaces differ, and all may be
+ * captured into CUDA graphs (so may awq_w4a16_matmul for M <= 16 and _packed, once a call of
+ * that shape has run). Every pointer is memory of one device, except where noted, the call
+ * runs there, and `stream` is one of its streams. Strides are in elements; the last dim is contiguous. They have no
+ * backward pass.
+ *
+ * awq_rms_norm ([AWQ-P1] section 6: the scales fold into the operation that produces the
+ * activations, so `weight` is w / s for an fp16 output that feeds awq_w4a16_matmul):
+ *   h = X + residual (fp32; h = X without one),  residual_out = h rounded to r_dtype,
+ *   y[m][k] = h[m][k] weight[k] / sqrt(mean_k h[m][k]^2 + eps)   (statistics in fp32, of the
+ *   unrounded h; rounded once to out_dtype)
+ * X [M][K], residual and residual_out [M][K] (may be NULL together; residual_out may be
+ * `residual` itself, otherwise it overlaps no other argument) and weight [K] each hold
+ * AWQ_DTYPE_F32, _F16 or _BF16; rows x_stride, r_stride and ro_stride apart. out [M][K]
+ * contiguous holds one of these types, or AWQ_DTYPE_E4M3: out_scales[m] = max_k |y| / 448 (1
+ * where that is zero) and out = e4m3(y / out_scales[m]); a row with a NaN or an infinity has
+ * a NaN scale. 0 <= M < 2^31 (0 does nothing), 1 <= K <= 57344. Rows of aligned 16-byte
+ * vectors (K % 8 == 0, K <= 16384) are the fast form. */
+int awq_rms_norm(const void* X, int x_dtype, int64_t x_stride, const void* residual, int r_dtype,
+                 int64_t r_stride, void* residual_out, int64_t ro_stride, const void* weight,
+                 int w_dtype, int64_t M, int64_t K, float eps, void* out, int out_dtype,
+                 float* out_scales, awq_stream_t stream);
+
+/* Frequencies of the position rotation, in radians per position, to HOST memory
+ * (rotary_dim / 2 doubles): f_i = base^(-2 i / rotary_dim), scaled for long contexts as
+ *   AWQ_ROPE_PLAIN   f_i
+ *   AWQ_ROPE_LINEAR  f_i / factor
+ *   AWQ_ROPE_BASE    base replaced by base * factor^(R / (R - 2)), R = rotary_dim
+ *   AWQ_ROPE_BANDS   t = original_len f_i / (2 pi) turns over the original length: f_i for
+ *                    t >= high, f_i / factor for t <= low, linear in t between
+ *   AWQ_ROPE_RAMP    the same two ends, linear in the pair's index between the pairs that turn
+ *                    `high` and `low` times (YaRN, Peng et al. 2023), with the magnitude
+ *                    0.1 ln(factor) + 1
+ * out_magnitude (may be NULL) receives the factor of the cosine and sine, 1 for the others. */
+enum { AWQ_ROPE_PLAIN = 0, AWQ_ROPE_LINEAR = 1, AWQ_ROPE_BASE = 2, AWQ_ROPE_BANDS = 3, AWQ_ROPE_RAMP = 4 };
+int awq_rope_frequencies(int rotary_dim, double base, int scaling, double factor,
+                         double original_len, double low, double high, double* out_freqs,
+                         double* out_magnitude);
+
+/* A paged key-value cache with the block table of a batch. Keys (and values) of sequence b
+ * at position p, head h lie at k + page * page_stride + (p % page_size) * slot_stride +
+ * h * head_stride, page = block_table[b * table_stride + p / page_size], head_dim elements
+ * each (64, 128 or 256), so any order of pages, slots and heads serves. Rows are 16-byte
+ * aligned. AWQ_DTYPE_F16, _BF16, or _E4M3 with one positive scale per head: value = scale *
+ * element. max_pages * page_size < 2^31 - 64. A page number outside 0 .. num_pages - 1 where
+ * one is needed is never followed; see the two operators. */
+typedef struct awq_paged_cache {
+  void* k;
+  void* v;
+  int64_t dtype, num_pages, page_size, heads, head_dim;
+  int64_t page_stride, slot_stride, head_stride;
+  const float* k_scale;       /* [heads], AWQ_DTYPE_E4M3 only */
+  const float* v_scale;
+  const int32_t* block_table; /* [n_seqs][max_pages] */
+  int64_t n_seqs, max_pages, table_stride;
+} awq_paged_cache;
+
+/* Token t of T, at positions[t] of sequence seqs[t] (seqs NULL: sequence t): writes
+ * q_out[t] = rotated q[t] ([T][Hq][D] contiguous, AWQ_DTYPE_F16 or _BF16) and the rotated k[t]
+ * and v[t] to the cache (e4m3: e4m3(x / scale), saturating at 448). q [T][Hq][D], k and v
+ * [T][heads][D] hold in_dtype (F32, F16 or BF16), rows 16-byte aligned, e.g. the three parts of
+ * one QKV product. Hq may be 0 (q, q_out unused). The pairs of dims (i, i + rotary_dim / 2),
+ * or (2 i, 2 i + 1) if `interleaved`, i < rotary_dim / 2, are turned by positions[t] * freqs[i]
+ * (DEVICE doubles; the product is taken in fp64) and multiplied by `magnitude`; dims from
+ * rotary_dim (a multiple of 16, at most D; 0 turns nothing) on are copied. A negative
+ * position is a padded row: its q_out is zeros and nothing is appended. A token whose
+ * sequence, position or page lies outside the table or the cache is not appended, its q_out
+ * is still written, and *status (device or pinned host memory, may be NULL) is set to
+ * AWQ_ERR_INVALID_ARG; *status is never cleared. Two tokens of a call must not name one
+ * place of the cache: what that place then holds is undefined. */
+int awq_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                  int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                  int64_t v_token_stride, int64_t v_head_stride, int in_dtype, int64_t T, int Hq,
+                  void* q_out, int q_dtype, const int32_t* positions, const int32_t* seqs,
+                  const double* freqs, int rotary_dim, int interleaved, float magnitude,
+                  const awq_paged_cache* cache, int32_t* status, awq_stream_t stream);
+
+/* One new token per sequence, b < n_seqs, over the first lengths[b] cached tokens (its own
+ * among them once appended):
+ *   out[b][h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q[b][h] . k_t - max)
+ * with the key-value head h / (Hq / heads). q [n_seqs][Hq][D] (AWQ_DTYPE_F16 or _BF16, of the
+ * cache's type if that has 16 bits; rows 16-byte aligned), out [n_seqs][Hq][D] contiguous of
+ * q's type. Scores, maximum and sums are fp32; the weights p_t enter the product with v in 16
+ * bits, and the sum that divides is of those. lengths[b] <= 0 gives zeros. A length beyond
+ * max_pages * page_size, or a needed page outside the cache, makes that sequence's output NaN
+ * and sets *status (device or pinned host memory, may be NULL, never cleared) to
+ * AWQ_ERR_INVALID_ARG. `workspace`: at least
+ * awq_paged_attention_workspace bytes of device memory (0 on bad arguments), 16-byte
+ * aligned, needing no initialisation; calls that may overlap need one each. */
+int64_t awq_paged_attention_workspace(int64_t n_seqs, int Hq, int Hkv, int head_dim);
+int awq_paged_attention(const void* q, int64_t q_seq_stride, int64_t q_head_stride, int q_dtype,
+                        int Hq, const awq_paged_cache* cache, const int32_t* lengths, float scale,
+                        void* out, void* workspace, int64_t workspace_bytes, int32_t* status,
+                        awq_stream_t stream);
 
 int awq_version(void);
 

@@ -8,6 +8,7 @@
 #include "../../include/awq_search.h"
 #include "awq_device.cuh"
 #include "awq_kernels.h"
+#include "decode_kernels.h"
 
 #include <cstdio>
 #include <cstdlib>
@@ -132,10 +133,14 @@ int validate(const void* X, const void* W, int in_dtype, int64_t M, int64_t K, i
 
 // Makes the device of `s` (or, for the legacy default stream, the device that owns
 // `ptr`) current for this library's runtime, so calls from any host thread and any
-// device work without a separate device-selection call.
+// device work without a separate device-selection call. A stream under capture cannot be
+// asked for its device (the question would end the capture): `ptr` answers for it too.
 void bind_device(cudaStream_t s, const void* ptr) {
   int dev = -1;
-  if (s != nullptr && cudaStreamGetDevice(s, &dev) != cudaSuccess) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (s != nullptr &&
+      (cudaStreamIsCapturing(s, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone ||
+       cudaStreamGetDevice(s, &dev) != cudaSuccess)) {
     cudaGetLastError();
     dev = -1;
   }
@@ -598,6 +603,25 @@ int search_device(const void* X, const void* W, int in_dtype, int64_t M, int64_t
 
 namespace awq {
 void record_error_message(const char* msg) { t_last_error = msg; }
+
+int decode_error(int status, const char* msg) {
+  t_last_error = msg;
+  return status;
+}
+int decode_cuda_error(cudaError_t e, const char* where) { return cuda_error(e, where); }
+int decode_device(const void* ptr, int* dev, int* num_sms) {
+  bind_device(nullptr, ptr);
+  return check_device(dev, num_sms);
+}
+bool decode_device_memory(const void* p, int dev) {
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return (at.type == cudaMemoryTypeDevice && at.device == dev) || at.type == cudaMemoryTypeManaged;
+}
+void record_launch_count(int launches) { g_last_launches = launches; }
 
 int search_in_workspace(const void* X, const void* W, int in_dtype, int64_t M, int64_t K, int64_t N, int group,
                         int n_grid, float* out_scales, int32_t* out_codes, void* out_steps, void* out_zeros,

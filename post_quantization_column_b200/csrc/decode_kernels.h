@@ -1,0 +1,167 @@
+// decode_kernels.h — the operators of a decode step around the W4A16 products (internal to
+// libawqsearch): the RMS norm that feeds a quantized layer, the append to a paged key-value
+// cache with the position rotation, and the attention of one new token over that cache.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "awq_kernels.h"
+
+namespace awq {
+
+// Element types of these operators (AWQ_DTYPE_* of the C ABI).
+enum : int { kTypeBf16 = 0, kTypeF32 = 1, kTypeF16 = 2, kTypeE4m3 = 3, kTypeNone = -1 };
+__host__ __device__ constexpr int type_bytes(int t) {
+  return t == kTypeF32 ? 4 : (t == kTypeE4m3 ? 1 : (t == kTypeNone ? 0 : 2));
+}
+constexpr float kE4m3Max = 448.0f;  // largest finite e4m3 value
+
+// ---- RMS norm ------------------------------------------------------------------------
+constexpr int64_t kNormMaxK = 57344;  // one fp32 row in shared memory
+struct NormArgs {
+  const void* X;             // [M][K], rows x_stride elements apart
+  const void* residual;      // [M][K] or NULL
+  void* residual_out;        // [M][K]; may be `residual`
+  const void* weight;        // [K]
+  void* out;                 // [M][K] contiguous
+  float* out_scales;         // [M], e4m3 output only
+  int64_t M, K, x_stride, r_stride, ro_stride;
+  int x_type, r_type, w_type, out_type;
+  float eps;
+};
+cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s, int* launches);
+
+// ---- paged key-value cache -------------------------------------------------------------
+// Element (page p, slot s, head h, dim d) of keys and of values lies at
+// p * page_stride + s * slot_stride + h * head_stride + d.
+struct PagedCache {
+  void* k;
+  void* v;
+  int64_t num_pages, page_stride, slot_stride, head_stride;
+  int page_size, heads, head_dim, type;
+  const float* k_scale;  // [heads], e4m3 only
+  const float* v_scale;
+  const int32_t* table;  // [seqs][max_pages], rows table_stride apart
+  int64_t seqs, max_pages, table_stride;
+};
+
+struct AppendArgs {
+  const void* q;  // [T][Hq][D], token and head strides in elements
+  const void* k;
+  const void* v;
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
+  int64_t T;
+  int Hq, in_type, q_type, rot, interleaved;
+  const double* freqs;       // [rot / 2] radians per position
+  float magnitude;
+  const int32_t* positions;  // [T]
+  const int32_t* seq;        // [T], NULL: token i belongs to sequence i
+  void* q_out;               // [T][Hq][D] contiguous
+  int32_t* status;           // may be NULL
+  PagedCache c;
+};
+cudaError_t launch_kv_append(const AppendArgs& a, int num_sms, cudaStream_t s, int* launches);
+
+struct PagedAttnArgs {
+  const void* q;  // [B][Hq][D]
+  int64_t q_sb, q_sh;
+  int64_t B;
+  int Hq, q_type;
+  const int32_t* lengths;  // [B]
+  float scale;
+  void* out;         // [B][Hq][D] contiguous, q's type
+  void* workspace;   // paged_attn_workspace bytes, 16-byte aligned
+  int32_t* status;   // may be NULL
+  PagedCache c;
+};
+int64_t paged_attn_workspace(int64_t B, int Hq, int Hkv, int D);
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* launches);
+
+// Shared with awq_api.cu: the entry points' error text, device selection and launch count.
+int decode_error(int status, const char* msg);
+int decode_cuda_error(cudaError_t e, const char* where);
+// Makes the device that owns `ptr` current and checks it.
+int decode_device(const void* ptr, int* dev, int* num_sms);
+bool decode_device_memory(const void* p, int dev);  // memory of device `dev`, or managed memory
+void record_launch_count(int launches);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float bits_f16(uint32_t h) { return __half2float(__ushort_as_half(static_cast<unsigned short>(h))); }
+// The two 16-bit values of a word as floats.
+__device__ __forceinline__ float2 unpack16(uint32_t w, int type) {
+  if (type == kTypeBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b, int type) {
+  if (type == kTypeBf16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two values rounded to e4m3 (finite values beyond +-448 saturate; NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float load_one(const void* p, int64_t i, int type) {
+  if (type == kTypeF32) return static_cast<const float*>(p)[i];
+  const uint32_t h = static_cast<const unsigned short*>(p)[i];
+  return type == kTypeBf16 ? __uint_as_float(h << 16) : bits_f16(h);
+}
+__device__ __forceinline__ void store_one(void* p, int64_t i, int type, float v) {
+  switch (type) {
+    case kTypeF32: static_cast<float*>(p)[i] = v; break;
+    case kTypeBf16: static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v); break;
+    case kTypeF16: static_cast<__half*>(p)[i] = __float2half_rn(v); break;
+    default: static_cast<uint8_t*>(p)[i] = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+  }
+}
+// Eight consecutive values (16-byte aligned; 8 bytes for e4m3) rounded to `type`.
+__device__ __forceinline__ void store8(void* p, int64_t i, int type, const float (&v)[8]) {
+  if (type == kTypeF32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    d[0] = make_float4(v[0], v[1], v[2], v[3]);
+    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else if (type == kTypeE4m3) {
+    const uint32_t lo = pack_e4m3(v[0], v[1]) | (pack_e4m3(v[2], v[3]) << 16);
+    const uint32_t hi = pack_e4m3(v[4], v[5]) | (pack_e4m3(v[6], v[7]) << 16);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + i) = make_uint2(lo, hi);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+        make_uint4(pack16(v[0], v[1], type), pack16(v[2], v[3], type), pack16(v[4], v[5], type),
+                   pack16(v[6], v[7], type));
+  }
+}
+// Eight consecutive 16- or 32-bit values (16-byte aligned) in their own form, read once.
+template <int BYTES>
+struct Raw8 {
+  uint4 w[BYTES / 2];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * BYTES);
+#pragma unroll
+    for (int k = 0; k < BYTES / 2; ++k) w[k] = s[k];
+  }
+  __device__ __forceinline__ void to_float(float (&v)[8], int type) const {
+    if constexpr (BYTES == 4) {
+      const uint4 a = w[0], b = w[BYTES / 2 - 1];
+      v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+      v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+    } else {
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack16(u[k], type);
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
+      }
+    }
+  }
+};
+#endif
+
+}  // namespace awq
