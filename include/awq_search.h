@@ -408,7 +408,8 @@ int awq_rope_frequencies(int rotary_dim, double base, int scaling, double factor
  * h * head_stride, page = block_table[b * table_stride + p / page_size], head_dim elements
  * each (64, 128 or 256), so any order of pages, slots and heads serves. Rows are 16-byte
  * aligned. AWQ_DTYPE_F16, _BF16, or _E4M3 with one positive scale per head: value = scale *
- * element. max_pages * page_size < 2^31 - 64. A page number outside 0 .. num_pages - 1 where
+ * element. max_pages * page_size < 2^31 - 1024; the
+ * keys, and the values, span less than 64 GB. A page number outside 0 .. num_pages - 1 where
  * one is needed is never followed; see the two operators. */
 typedef struct awq_paged_cache {
   void* k;

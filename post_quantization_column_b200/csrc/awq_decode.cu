@@ -46,7 +46,7 @@ int take_cache(const awq_paged_cache* in, PagedCache* out) {
   if (in->heads < 1 || in->heads > 65535 || in->page_size < 1 || in->num_pages < 1 || in->n_seqs < 1 ||
       in->max_pages < 1 || in->page_size > kIntMax || in->num_pages > kIntMax || in->n_seqs > kIntMax)
     return decode_error(AWQ_ERR_SHAPE, "heads, page_size, num_pages, n_seqs and max_pages must be positive");
-  if (in->max_pages > (kIntMax - 64) / in->page_size)
+  if (in->max_pages > (kIntMax - 1024) / in->page_size)
     return decode_error(AWQ_ERR_SHAPE, "a block table row names 2^31 tokens or more");
   const int64_t per16 = 16 / type_bytes(static_cast<int>(in->dtype));
   if (!aligned(in->k, 16) || !aligned(in->v, 16) || in->page_stride % per16 || in->slot_stride % per16 ||
@@ -54,6 +54,16 @@ int take_cache(const awq_paged_cache* in, PagedCache* out) {
     return decode_error(AWQ_ERR_INVALID_ARG, "the cache's rows must be 16-byte aligned");
   if (in->page_stride < 0 || in->slot_stride < 0 || in->head_stride < 0 || in->table_stride < 0)
     return decode_error(AWQ_ERR_INVALID_ARG, "strides must not be negative");
+  // places within the cache are counted in units of 16 bytes, in 32 bits; a division keeps the
+  // check itself from overflowing
+  const int64_t room = ((int64_t(1) << 32) - 2) * per16 - in->head_dim, steps[3] = {in->num_pages - 1, in->page_size - 1, in->heads - 1};
+  const int64_t strides[3] = {in->page_stride, in->slot_stride, in->head_stride};
+  int64_t span = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (steps[i] > 0 && strides[i] > (room - span) / steps[i])
+      return decode_error(AWQ_ERR_SHAPE, "the keys or the values of a cache span 64 GB or more");
+    span += steps[i] * strides[i];
+  }
   if (!aligned(in->block_table, 4) || !aligned(in->k_scale, 4) || !aligned(in->v_scale, 4))
     return decode_error(AWQ_ERR_INVALID_ARG, "the block table or a scale is misaligned");
   out->k = in->k;

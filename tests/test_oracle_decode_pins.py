@@ -107,7 +107,7 @@ CACHE = dict(k=P, v=P, dtype=2, num_pages=4, page_size=16, heads=2, head_dim=128
 BAD_CACHES = ((dict(k=0), 1), (dict(v=0), 1), (dict(table=0), 1), (dict(dtype=1), 1), (dict(dtype=3), 1), (dict(head_dim=80), 2),
               (dict(heads=0), 2), (dict(page_size=0), 2), (dict(num_pages=0), 2), (dict(seqs=0), 2), (dict(max_pages=0), 2),
               (dict(max_pages=1 << 30), 2), (dict(k=P + 8), 1), (dict(ps=4097), 1), (dict(ss=4), 1), (dict(hs=-128), 1),
-              (dict(table=P + 2), 1), (dict(num_pages=1 << 31), 2))
+              (dict(table=P + 2), 1), (dict(num_pages=1 << 31), 2), (dict(ps=1 << 34), 2), (dict(ps=1 << 62), 2))
 
 
 def _cache(**kw):
