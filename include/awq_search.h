@@ -406,10 +406,10 @@ int awq_rope_frequencies(int rotary_dim, double base, int scaling, double factor
 /* A paged key-value cache with the block table of a batch. Keys (and values) of sequence b
  * at position p, head h lie at k + page * page_stride + (p % page_size) * slot_stride +
  * h * head_stride, page = block_table[b * table_stride + p / page_size], head_dim elements
- * each (64, 128 or 256), so any order of pages, slots and heads serves. Rows are 16-byte
+ * each (64, 128 or 256), so any order of pages, slots and heads serves. Rows are 32-byte
  * aligned. AWQ_DTYPE_F16, _BF16, or _E4M3 with one positive scale per head: value = scale *
  * element. max_pages * page_size < 2^31 - 1024; the
- * keys, and the values, span less than 64 GB. A page number outside 0 .. num_pages - 1 where
+ * keys, and the values, span less than 128 GB. A page number outside 0 .. num_pages - 1 where
  * one is needed is never followed; see the two operators. */
 typedef struct awq_paged_cache {
   void* k;
@@ -454,7 +454,7 @@ int awq_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, 
  * AWQ_ERR_INVALID_ARG. `workspace`: at least
  * awq_paged_attention_workspace bytes of device memory (0 on bad arguments), 16-byte
  * aligned, needing no initialisation; calls that may overlap need one each. */
-int64_t awq_paged_attention_workspace(int64_t n_seqs, int Hq, int Hkv, int head_dim);
+int64_t awq_paged_attention_workspace(int Hq, int Hkv, int head_dim, int cache_dtype);
 int awq_paged_attention(const void* q, int64_t q_seq_stride, int64_t q_head_stride, int q_dtype,
                         int Hq, const awq_paged_cache* cache, const int32_t* lengths, float scale,
                         void* out, void* workspace, int64_t workspace_bytes, int32_t* status,

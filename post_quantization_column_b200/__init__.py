@@ -130,7 +130,7 @@ def library() -> ctypes.CDLL:
     lib.awq_rope_frequencies.argtypes = [c32, f64, c32, f64, f64, f64, f64, vp, ctypes.POINTER(ctypes.c_double)]
     lib.awq_kv_append.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, i64, i32, vp, i32, vp, vp, vp, i32, i32,
                                   f32, vp, vp, vp]
-    lib.awq_paged_attention_workspace.argtypes = [i64, i32, i32, i32]
+    lib.awq_paged_attention_workspace.argtypes = [i32, i32, i32, i32]
     lib.awq_paged_attention_workspace.restype = ctypes.c_int64
     lib.awq_paged_attention.argtypes = [vp, i64, i64, i32, i32, vp, vp, f32, vp, vp, i64, vp, vp]
     for name in ("awq_rms_norm", "awq_rope_frequencies", "awq_kv_append", "awq_paged_attention"):
@@ -932,7 +932,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise ValueError("lengths must be (sequences,) contiguous int32")
     q = _rows16(q, "q", Hq, D)
     lib = library()
-    size = lib.awq_paged_attention_workspace(B, Hq, heads, D)
+    size = lib.awq_paged_attention_workspace(Hq, heads, D, _DTYPES[k_cache.dtype])
     out = torch.empty(B, Hq, D, dtype=q.dtype, device=device)
     ws = torch.empty(size, dtype=torch.uint8, device=device)
     st_ptr = _status_ptr(status, device)

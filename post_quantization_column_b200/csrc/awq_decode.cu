@@ -48,20 +48,20 @@ int take_cache(const awq_paged_cache* in, PagedCache* out) {
     return decode_error(AWQ_ERR_SHAPE, "heads, page_size, num_pages, n_seqs and max_pages must be positive");
   if (in->max_pages > (kIntMax - 1024) / in->page_size)
     return decode_error(AWQ_ERR_SHAPE, "a block table row names 2^31 tokens or more");
-  const int64_t per16 = 16 / type_bytes(static_cast<int>(in->dtype));
-  if (!aligned(in->k, 16) || !aligned(in->v, 16) || in->page_stride % per16 || in->slot_stride % per16 ||
-      in->head_stride % per16)
-    return decode_error(AWQ_ERR_INVALID_ARG, "the cache's rows must be 16-byte aligned");
+  const int64_t per32 = 32 / type_bytes(static_cast<int>(in->dtype));
+  if (!aligned(in->k, 32) || !aligned(in->v, 32) || in->page_stride % per32 || in->slot_stride % per32 ||
+      in->head_stride % per32)
+    return decode_error(AWQ_ERR_INVALID_ARG, "the cache's rows must be 32-byte aligned");
   if (in->page_stride < 0 || in->slot_stride < 0 || in->head_stride < 0 || in->table_stride < 0)
     return decode_error(AWQ_ERR_INVALID_ARG, "strides must not be negative");
-  // places within the cache are counted in units of 16 bytes, in 32 bits; a division keeps the
+  // places within the cache are counted in units of 32 bytes, in 32 bits; a division keeps the
   // check itself from overflowing
-  const int64_t room = ((int64_t(1) << 32) - 2) * per16 - in->head_dim, steps[3] = {in->num_pages - 1, in->page_size - 1, in->heads - 1};
+  const int64_t room = ((int64_t(1) << 32) - 2) * per32 - in->head_dim, steps[3] = {in->num_pages - 1, in->page_size - 1, in->heads - 1};
   const int64_t strides[3] = {in->page_stride, in->slot_stride, in->head_stride};
   int64_t span = 0;
   for (int i = 0; i < 3; ++i) {
     if (steps[i] > 0 && strides[i] > (room - span) / steps[i])
-      return decode_error(AWQ_ERR_SHAPE, "the keys or the values of a cache span 64 GB or more");
+      return decode_error(AWQ_ERR_SHAPE, "the keys or the values of a cache span 128 GB or more");
     span += steps[i] * strides[i];
   }
   if (!aligned(in->block_table, 4) || !aligned(in->k_scale, 4) || !aligned(in->v_scale, 4))
@@ -251,9 +251,11 @@ int awq_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, 
   return AWQ_OK;
 }
 
-int64_t awq_paged_attention_workspace(int64_t B, int Hq, int Hkv, int head_dim) {
-  if (B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || (head_dim != 64 && head_dim != 128 && head_dim != 256)) return 0;
-  return paged_attn_workspace(B, Hq, Hkv, head_dim);
+int64_t awq_paged_attention_workspace(int Hq, int Hkv, int head_dim, int cache_dtype) {
+  if (Hkv < 1 || Hq < Hkv || Hq % Hkv || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+      (cache_dtype != kTypeBf16 && cache_dtype != kTypeF16 && cache_dtype != kTypeE4m3))
+    return 0;
+  return paged_attn_workspace(Hq, Hkv, head_dim, cache_dtype);
 }
 
 int awq_paged_attention(const void* q, int64_t q_seq_stride, int64_t q_head_stride, int q_dtype, int Hq,
@@ -275,7 +277,7 @@ int awq_paged_attention(const void* q, int64_t q_seq_stride, int64_t q_head_stri
     return decode_error(AWQ_ERR_INVALID_ARG, "q, out and the work space must be 16-byte aligned");
   if (q_seq_stride < 0 || q_head_stride < 0) return decode_error(AWQ_ERR_INVALID_ARG, "strides must not be negative");
   if (!aligned(lengths, 4) || !aligned(status, 4)) return decode_error(AWQ_ERR_INVALID_ARG, "lengths or status is misaligned");
-  if (workspace_bytes < awq_paged_attention_workspace(a.c.seqs, Hq, a.c.heads, a.c.head_dim))
+  if (workspace_bytes < awq_paged_attention_workspace(Hq, a.c.heads, a.c.head_dim, a.c.type))
     return decode_error(AWQ_ERR_INVALID_ARG, "the work space is smaller than awq_paged_attention_workspace says");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DeviceRestore restore_device;

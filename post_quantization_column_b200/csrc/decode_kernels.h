@@ -78,7 +78,7 @@ struct PagedAttnArgs {
   int32_t* status;   // may be NULL
   PagedCache c;
 };
-int64_t paged_attn_workspace(int64_t B, int Hq, int Hkv, int D);
+int64_t paged_attn_workspace(int Hq, int Hkv, int D, int type);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* launches);
 
 // Shared with awq_api.cu: the entry points' error text, device selection and launch count.

@@ -37,16 +37,19 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCtas = 3 * 148;  // three CTAs on each of a B200's SMs
 
 template <int D, int TYPE, int NB>
 struct Tile {
   static constexpr int ES = type_bytes(TYPE);
-  static constexpr int kKChunks = D * ES / 64;                       // 16-byte pieces per key row and lane
-  static constexpr int kVBytes = D * ES / 8 < 16 ? D * ES / 8 : 16;  // bytes of a piece of a value row
-  static constexpr int kVChunks = D * ES / 8 / kVBytes;              // pieces per value row and lane
+  static constexpr int kKBytes = D * ES / 4 < 32 ? D * ES / 4 : 32;  // bytes of a lane's piece of a key row (4 lanes a row)
+  static constexpr int kKChunks = D * ES / 4 / kKBytes;              // pieces per key row and lane
+  static constexpr int kVBytes = D * ES / 8 < 32 ? D * ES / 8 : 32;  // the same of a value row (8 lanes a row)
+  static constexpr int kVChunks = D * ES / 8 / kVBytes;
   static constexpr int kSteps = D / 16;                              // k16 steps of q . k; also tiles of 16 dims of O^T
   static constexpr int kBlocks = 256 / (D * ES) > 1 ? 256 / (D * ES) : 1;  // blocks of 16 tokens of a warp's tile
-  static constexpr int kUnit = kWarps * 16 * kBlocks;                // tokens of a unit
+  static constexpr int kTok = 16 * kBlocks;
+  static constexpr bool kShort = D * ES <= 128;                      // rows of which a CTA may take several heads'
   static constexpr int kHeads = NB * 8;                              // query heads of a work segment
   static constexpr int kPitch = D + 2;                               // floats between heads in the join buffer
   static constexpr int kCtas = D * NB > 128 || (D == 64 && NB == 2) ? 2 : 3;                // per SM, by registers
@@ -89,7 +92,11 @@ template <int BYTES>
 struct Piece {
   uint32_t w[BYTES / 4];
   __device__ __forceinline__ void load(const uint8_t* p) {
-    if constexpr (BYTES == 16)
+    if constexpr (BYTES == 32)
+      asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "l"(p));
+    else if constexpr (BYTES == 16)
       asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                    : "l"(p));
@@ -101,6 +108,13 @@ struct Piece {
     for (int i = 0; i < BYTES / 4; ++i) w[i] = 0u;
   }
 };
+
+// `from` + 32 `place`.
+__device__ __forceinline__ const uint8_t* at_place(const uint8_t* from, uint32_t place) {
+  uint64_t p;
+  asm("mad.wide.u32 %0, %1, 32, %2;" : "=l"(p) : "r"(place), "l"(from));
+  return reinterpret_cast<const uint8_t*>(p);
+}
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -117,38 +131,43 @@ __device__ __forceinline__ int clamped_length(const int32_t* lengths, int64_t b,
 __host__ __device__ __forceinline__ int64_t run_start(int64_t c, int64_t T, int64_t C) { return c * T / C; }
 __device__ __forceinline__ int64_t unit_owner(int64_t l, int64_t T, int64_t C) { return ((l + 1) * C - 1) / T; }
 
-constexpr uint32_t kNoRow = 0xFFFFFFFFu;        // a row without a place (a place of the last 16 bytes below 64 GB)
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;        // a row without a place (the last 32 bytes below 128 GB)
 constexpr float kNoMax = -3.402823466e38f;  // the maximum before any score: finite, so that m - m is 0
 
-// A place in the sequence-major list of units: sequence, (key-value head, head block), unit.
+// A place in the sequence-major list of units: sequence, group of key-value heads, block of their
+// query heads, unit.
 struct Cursor {
-  int b, kvh, hg, blk, len;
+  int b, kg, hg, blk, len;
 };
 
 struct Space {       // the work space of a launch
   float* o;          // [2 C][heads][D] partial sums of run c: slot 2 c of the segment that begins in it and
                      // goes on, slot 2 c + 1 of the one that began before it
   float2* ml;        // [2 C][heads] (m, l)
-  int64_t* prefix;   // [B + 1] units per (key-value head, head block) before each sequence
+  int4* joins;       // what the second kernel joins: pieces (0: nothing), first run, sequence, head block;
+                     // one per segment if there are no more segments than CTAs, else one per CTA
 };
 
 struct Geometry {
   int cap;           // tokens a table row can name
   int heads_per;     // Hq / Hkv
-  int hgroups;       // head blocks per key-value head
+  int hgroups;       // blocks of query heads per key-value head
+  int side;          // key-value heads side by side in a CTA: 1, 2 or 4, of kWarps / side warps each
   int64_t ctas;
-  uint32_t page16, slot16, head16;  // the cache's strides in units of 16 bytes
+  int by_segment;    // the joins are listed by segment
+  int64_t listed;
+  uint32_t page32, slot32, head32;  // the cache's strides in units of 32 bytes
   uint32_t page_mul;  // p / page_size = (p * page_mul) >> page_shift for 0 <= p < 2^31
   int page_shift;
-  int block_pages;    // every block of 16 tokens lies in one page
 };
 
-template <int D, int TYPE, int NB>
+// WHOLE: every block of 16 tokens lies in one page (the page size is a multiple of 16).
+template <int D, int TYPE, int NB, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
     paged_attn_kernel(PagedAttnArgs a, Geometry geo, Space sp) {
   using T_ = Tile<D, TYPE, NB>;
-  constexpr int ES = T_::ES, KC = T_::kKChunks, VB = T_::kVBytes, VC = T_::kVChunks, S = T_::kSteps, TB = T_::kBlocks;
-  constexpr int kUnit = T_::kUnit, kTok = 16 * TB;
+  constexpr int ES = T_::ES, KB = T_::kKBytes, KC = T_::kKChunks, VB = T_::kVBytes, VC = T_::kVChunks, S = T_::kSteps, TB = T_::kBlocks;
+  constexpr int kTok = T_::kTok;
   constexpr int MMA = TYPE == kTypeBf16 ? kTypeBf16 : kTypeF16;
   // The maximum in use may lag behind the scores by 2^kLag before the sums are rescaled: weights
   // are p 2^kBias, 2^(kBias + kLag) at most, and in fp16 stay representable down to p = 2^-31 of
@@ -162,12 +181,16 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t = lane & 3;
   const PagedCache& c = a.c;
-  const int HH = c.heads * geo.hgroups;
+  const int side = T_::kShort ? geo.side : 1, unit = kTok * kWarps / side;
+  const int HH = c.heads / side * geo.hgroups;
+  const int deep = kWarps / side, head_of = warp / deep, tok_of = warp % deep * kTok;  // the warp's head and tokens of a unit
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join is set up meanwhile
 
   // ---- the run: exclusive sums of the sequences' units, then the sequence of its first unit
   const int64_t per = ceil_div(a.B, kThreads), b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   int64_t mine = 0;
-  for (int64_t b = b0; b < b1; ++b) mine += (clamped_length(a.lengths, b, geo.cap) + kUnit - 1) / kUnit;
+  for (int64_t b = b0; b < b1; ++b) mine += (clamped_length(a.lengths, b, geo.cap) + unit - 1) / unit;
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -181,14 +204,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
     if (w < warp) before += sScan[w];
     total += sScan[w];
   }
-  if (blockIdx.x == 0) {
-    int64_t at = before;
-    for (int64_t b = b0; b < b1; ++b) {
-      sp.prefix[b] = at;
-      at += (clamped_length(a.lengths, b, geo.cap) + kUnit - 1) / kUnit;
-    }
-    if (tid == 0) sp.prefix[a.B] = total;
-  }
   // no run is empty: with fewer units than CTAs the later CTAs have none
   const int64_t units = total * HH, C = min(geo.ctas, units);
   const int64_t u0 = blockIdx.x < C ? run_start(blockIdx.x, units, C) : 0;
@@ -196,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   if (n > 0 && before * HH <= u0 && u0 < (before + mine) * HH) {
     int64_t at = before * HH;
     for (int64_t b = b0; b < b1; ++b) {
-      const int len = clamped_length(a.lengths, b, geo.cap), nblk = (len + kUnit - 1) / kUnit;
+      const int len = clamped_length(a.lengths, b, geo.cap), nblk = (len + unit - 1) / unit;
       if (u0 < at + static_cast<int64_t>(nblk) * HH) {
         const int64_t rel = u0 - at;
         const int hh = static_cast<int>(rel / nblk);
@@ -208,19 +223,25 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   }
   // sequences without tokens have no units: their rows of zeros are dealt out too
   for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x)
-    if (__ldg(a.lengths + b) <= 0)
+    if (__ldg(a.lengths + b) <= 0) {
+      if (geo.by_segment)
+        for (int i = tid; i < HH; i += kThreads) sp.joins[b * HH + i] = make_int4(0, 0, 0, 0);
       for (int64_t i = tid; i < static_cast<int64_t>(a.Hq) * D / 2; i += kThreads)
         static_cast<uint32_t*>(a.out)[b * a.Hq * D / 2 + i] = 0u;
+    }
+  if (n == 0) {
+    if (tid == 0 && !geo.by_segment) sp.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
   __syncthreads();
-  if (n == 0) return;
 
   auto advance = [&](Cursor& k) {
-    if (++k.blk * kUnit < k.len) return;
+    if (++k.blk * unit < k.len) return;
     k.blk = 0;
     if (++k.hg < geo.hgroups) return;
     k.hg = 0;
-    if (++k.kvh < c.heads) return;
-    k.kvh = 0;
+    if (++k.kg < c.heads / side) return;
+    k.kg = 0;
     do {
       ++k.b;
       k.len = k.b < a.B ? clamped_length(a.lengths, k.b, geo.cap) : 1;
@@ -228,86 +249,113 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   };
 
   // ---- the loading side. look_up() asks the block table for a tile's pages one tile before
-  // place() turns them into places of the cache, in units of 16 bytes: per block of 16 tokens
-  // that of its first row where blocks lie in one page, of row lane % 16 otherwise.
+  // place() turns them into places of the cache, in units of 32 bytes: per block of 16 tokens
+  // that of its first row if WHOLE, of row lane % 16 otherwise.
   Cursor ic = sStart;
   int looked = 0;
-  int32_t page[TB];        // asked for
-  uint32_t row[TB];        // placed
+  int32_t page[TB];            // asked for
+  uint32_t within[TB];         // places from the page's to the row's
+  uint32_t row[TB];            // placed
   int ask_rows = 0, rows = 0;  // rows left of the sequence from the tile's first on
-  int ask_tok = 0;
-  uint32_t ask_head = 0;
-  bool full = false;       // every block of the placed tile has its 16 rows, in one page
-  bool bad_tile = false;   // the placed tile needs a page outside the cache
-  auto page_of = [&](int tok) { return static_cast<int>(static_cast<uint64_t>(tok) * geo.page_mul >> geo.page_shift); };
+  bool full = false;           // every block of the placed tile has its 16 rows
+  bool bad_tile = false;       // the placed tile needs a page outside the cache
+  const int own = WHOLE ? 0 : lane & 15;
   auto look_up = [&]() {
     if (looked >= n) {
       ask_rows = 0;
     } else {
       if (looked > 0) advance(ic);
-      ask_rows = ic.len - (ic.blk * kUnit + warp * kTok);
+      ask_rows = ic.len - (ic.blk * unit + tok_of);
     }
     ++looked;
-    ask_tok = ic.blk * kUnit + warp * kTok + (geo.block_pages ? 0 : lane & 15);
-    ask_head = ic.kvh * geo.head16;
+    const int tok0 = ic.blk * unit + tok_of + own;
     const int32_t* table = c.table + ic.b * c.table_stride;
 #pragma unroll
     for (int k = 0; k < TB; ++k) {
+      const int tok = tok0 + 16 * k;
+      const uint32_t pi = static_cast<uint32_t>(static_cast<uint64_t>(tok) * geo.page_mul >> geo.page_shift);
+      within[k] = (tok - pi * c.page_size) * geo.slot32 + (ic.kg * side + head_of) * geo.head32;
       page[k] = -1;
-      if (16 * k + (geo.block_pages ? 0 : lane & 15) < ask_rows) page[k] = __ldg(table + page_of(ask_tok + 16 * k));
+      if (16 * k + own < ask_rows) page[k] = __ldg(table + pi);
     }
   };
   auto place = [&]() {
     rows = ask_rows;
-    full = geo.block_pages && rows >= kTok;
-    bad_tile = false;
+    bool inside = true;
 #pragma unroll
     for (int k = 0; k < TB; ++k) {
-      const int tok = ask_tok + 16 * k;
-      const bool inside = static_cast<uint32_t>(page[k]) < static_cast<uint32_t>(c.num_pages);
-      row[k] = inside ? static_cast<uint32_t>(page[k]) * geo.page16 +
-                            static_cast<uint32_t>(tok - page_of(tok) * c.page_size) * geo.slot16 + ask_head
-                      : kNoRow;
-      full = full && inside;
-      bad_tile = bad_tile || (!inside && 16 * k + (geo.block_pages ? 0 : lane & 15) < rows);
+      const bool in = static_cast<uint32_t>(page[k]) < static_cast<uint32_t>(c.num_pages);
+      row[k] = in ? page[k] * geo.page32 + within[k] : kNoRow;
+      inside = inside && in;
     }
+    full = WHOLE && inside && rows >= kTok;
+    bad_tile = false;
+    if (!inside)
+#pragma unroll
+      for (int k = 0; k < TB; ++k) bad_tile = bad_tile || (row[k] == kNoRow && 16 * k + own < rows);
   };
-  Piece<16> kr[TB][2][KC];
+  Piece<KB> kr[TB][2][KC];
   Piece<VB> vr[TB][4][VC];
-  // Loads the lane's rows of a tile: its row r of a block is token at(r), its bytes from `from` on.
-  auto load_tile = [&](const uint8_t* from, auto at, auto& piece) {
-    constexpr int ROWS = sizeof(piece[0]) / sizeof(piece[0][0]);
-    constexpr int PIECES = sizeof(piece[0][0]) / sizeof(piece[0][0][0]);
-    constexpr int STEP = ROWS == 2 ? 64 : 8 * static_cast<int>(sizeof(piece[0][0][0]));
+  // The lane's rows of a block: tokens g, g + 8 of the keys, 2t, 2t + 1, 2t + 8, 2t + 9 of the values.
+  uint32_t k_at[2], v_at[4];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) k_at[r] = (g + 8 * r) * geo.slot32;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v_at[r] = (2 * t + (r & 1) + 8 * (r >> 1)) * geo.slot32;
+  const uint8_t* k_from = static_cast<const uint8_t*>(c.k) + KB * t;
+  const uint8_t* v_from = static_cast<const uint8_t*>(c.v) + VB * g;
+  auto load_keys = [&]() {
     if (full) {
 #pragma unroll
       for (int k = 0; k < TB; ++k)
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          const uint8_t* src = from + static_cast<uint64_t>(row[k] + at(r) * geo.slot16) * 16u;
+        for (int r = 0; r < 2; ++r) {
+          const uint8_t* src = at_place(k_from, row[k] + k_at[r]);
 #pragma unroll
-          for (int j = 0; j < PIECES; ++j) piece[k][r][j].load(src + STEP * j);
+          for (int j = 0; j < KC; ++j) kr[k][r][j].load(src + 4 * KB * j);
         }
       return;
     }
 #pragma unroll
     for (int k = 0; k < TB; ++k)
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        uint32_t off = __shfl_sync(~0u, row[k], at(r));
-        if (geo.block_pages)
-          off = row[k] != kNoRow && 16 * k + static_cast<int>(at(r)) < rows ? row[k] + at(r) * geo.slot16 : kNoRow;
+      for (int r = 0; r < 2; ++r) {
+        const int tok = g + 8 * r;
+        const uint32_t off = WHOLE ? row[k] + k_at[r] : __shfl_sync(~0u, row[k], tok);
+        const bool live = (WHOLE ? row[k] : off) != kNoRow && 16 * k + tok < rows;
 #pragma unroll
-        for (int j = 0; j < PIECES; ++j) {
-          piece[k][r][j].zero();
-          if (off != kNoRow) piece[k][r][j].load(from + static_cast<uint64_t>(off) * 16u + STEP * j);
+        for (int j = 0; j < KC; ++j) {
+          kr[k][r][j].zero();
+          if (live) kr[k][r][j].load(at_place(k_from, off) + 4 * KB * j);
         }
       }
   };
-  const uint8_t* k_from = static_cast<const uint8_t*>(c.k) + 16 * t;
-  const uint8_t* v_from = static_cast<const uint8_t*>(c.v) + VB * g;
-  auto load_keys = [&]() { load_tile(k_from, [&](uint32_t r) { return g + 8 * r; }, kr); };
-  auto load_values = [&]() { load_tile(v_from, [&](uint32_t r) { return 2 * t + (r & 1) + 8 * (r >> 1); }, vr); };
+  auto load_values = [&]() {
+    if (full) {
+#pragma unroll
+      for (int k = 0; k < TB; ++k)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint8_t* src = at_place(v_from, row[k] + v_at[r]);
+#pragma unroll
+          for (int j = 0; j < VC; ++j) vr[k][r][j].load(src + 8 * VB * j);
+        }
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < TB; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int tok = 2 * t + (r & 1) + 8 * (r >> 1);
+        const uint32_t off = WHOLE ? row[k] + v_at[r] : __shfl_sync(~0u, row[k], tok);
+        const bool live = (WHOLE ? row[k] : off) != kNoRow && 16 * k + tok < rows;
+#pragma unroll
+        for (int j = 0; j < VC; ++j) {
+          vr[k][r][j].zero();
+          if (live) vr[k][r][j].load(at_place(v_from, off) + 8 * VB * j);
+        }
+      }
+  };
   look_up();
   place();
   load_keys();
@@ -326,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
     if (fresh) {  // a segment of the run begins
       fresh = false;
       bad = __ldg(a.lengths + cc.b) > geo.cap;
-      const int kvh = cc.kvh, hb = cc.hg * T_::kHeads;
+      const int kvh = cc.kg * side + head_of, hb = cc.hg * T_::kHeads;
       const float k_scale = TYPE == kTypeE4m3 ? __ldg(c.k_scale + kvh) : 1.0f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -338,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
 #pragma unroll
         for (int st = 0; st < S; ++st) {
           // dims of step st: 4 elements of the lane's piece st / PER
-          constexpr int PER = 4 / ES;  // steps a 16-byte piece serves: 2 (16 bits) or 4 (8 bits)
-          const int d = (st / PER) * (64 / ES) + (16 / ES) * t + 4 * (st % PER);
+          constexpr int PER = KB / (4 * ES);  // steps that a piece serves
+          const int d = (st / PER) * (4 * KB / ES) + (KB / ES) * t + 4 * (st % PER);
           const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(q + d)) : make_uint2(0u, 0u);
           qf[nb][st][0] = w.x ^ flip;
           qf[nb][st][1] = w.y ^ flip;
@@ -382,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
       }
     }
     bad = bad || bad_now;
-    const int tok0 = cc.blk * kUnit + warp * kTok;
+    const int tok0 = cc.blk * unit + tok_of;
     // one block and one group of heads: two chains of products, for their latency
     constexpr int CHAINS = TB * NB == 1 ? 2 : 1;
     float s[TB][NB][4];
@@ -396,24 +444,25 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
           for (int h = 0; h < CHAINS; ++h) s2[h][k][nb][0] = s2[h][k][nb][1] = s2[h][k][nb][2] = s2[h][k][nb][3] = 0.0f;
 #pragma unroll
         for (int j = 0; j < KC; ++j) {
-          const uint32_t(&wl)[4] = kr[k][0][j].w;  // row g
-          const uint32_t(&wh)[4] = kr[k][1][j].w;  // row g + 8
+          const auto& wl = kr[k][0][j].w;  // row g
+          const auto& wh = kr[k][1][j].w;  // row g + 8
+          constexpr int PER = KB / (4 * ES);
           if constexpr (ES == 2) {
 #pragma unroll
-            for (int st = 0; st < 2; ++st)
+            for (int st = 0; st < PER; ++st)
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
-                mma_16816<MMA>(s2[st % CHAINS][k][nb], wl[2 * st], wh[2 * st], wl[2 * st + 1], wh[2 * st + 1], qf[nb][2 * j + st][0],
-                               qf[nb][2 * j + st][1]);
+                mma_16816<MMA>(s2[st % CHAINS][k][nb], wl[2 * st], wh[2 * st], wl[2 * st + 1], wh[2 * st + 1], qf[nb][PER * j + st][0],
+                               qf[nb][PER * j + st][1]);
           } else {
 #pragma unroll
-            for (int st = 0; st < 4; ++st) {
+            for (int st = 0; st < PER; ++st) {
               uint32_t a0, a1, a2, a3;
               e4m3_pairs(wl[st], a0, a2);
               e4m3_pairs(wh[st], a1, a3);
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
-                mma_16816<MMA>(s2[st % CHAINS][k][nb], a0, a1, a2, a3, qf[nb][4 * j + st][0], qf[nb][4 * j + st][1]);
+                mma_16816<MMA>(s2[st % CHAINS][k][nb], a0, a1, a2, a3, qf[nb][PER * j + st][0], qf[nb][PER * j + st][1]);
             }
           }
         }
@@ -517,10 +566,9 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
     bad_now = bad_tile;
     look_up();
 
-    const bool ends = (cc.blk + 1) * kUnit >= cc.len, last = i + 1 == n;
+    const bool ends = (cc.blk + 1) * unit >= cc.len, last = i + 1 == n;
     if (ends || last) {
       // ---- the four warps meet: factors to the common maximum, then one sum per head and dim
-      if (last) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -536,10 +584,24 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
       const int64_t seg0 = u0 + i - cc.blk;  // the segment's first unit
       const bool whole = ends && seg0 >= u0;
       const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (seg0 < u0 ? 1 : 0);
-      const int kvh = cc.kvh, hb = cc.hg * T_::kHeads;
+      const int hb = cc.hg * T_::kHeads;
       const int live = min(T_::kHeads, geo.heads_per - hb);
-      const float v_scale = TYPE == kTypeE4m3 ? __ldg(c.v_scale + kvh) : 1.0f;
-      if (any_bad && tid == 0 && a.status) *a.status = 1;
+      if (tid == 0) {
+        if (any_bad && a.status) *a.status = 1;
+        const bool begins = seg0 >= u0;
+        if (geo.by_segment ? begins : last) {
+          const int hh = cc.kg * geo.hgroups + cc.hg;
+          int pieces = 0;
+          if (begins && !ends)
+            pieces = static_cast<int>(unit_owner(seg0 + (cc.len + unit - 1) / unit - 1, units, C) - blockIdx.x) + 1;
+          sp.joins[geo.by_segment ? static_cast<int64_t>(cc.b) * HH + hh : blockIdx.x] = make_int4(pieces, blockIdx.x, cc.b, hh);
+        }
+      }
+      auto top_of = [&](int hs, int h) {  // the maximum of head h of the hs-th key-value head
+        float top = sM[hs * deep][h];
+        for (int w = hs * deep + 1; w < (hs + 1) * deep; ++w) top = fmaxf(top, sM[w][h]);
+        return top;
+      };
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         if (nb) __syncthreads();
@@ -547,8 +609,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
         for (int x = 0; x < 2; ++x) {
           const int h = nb * 8 + 2 * t + x;
           if (h < live) {
-            const float top = fmaxf(fmaxf(sM[0][h], sM[1][h]), fmaxf(sM[2][h], sM[3][h]));
-            const float f = exp2f(m[nb][x] - top);
+            const float f = exp2f(m[nb][x] - top_of(head_of, h));
             float* dst = join_buf + (warp * 8 + 2 * t + x) * T_::kPitch;
 #pragma unroll
             for (int st = 0; st < S; ++st) {
@@ -559,12 +620,12 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
           }
         }
         __syncthreads();
-        for (int e = tid; e < min(8, live - nb * 8) * (D / 4); e += kThreads) {
-          const int h8 = e / (D / 4), d = (e % (D / 4)) * 4, h = nb * 8 + h8;
-          const float top = fmaxf(fmaxf(sM[0][h], sM[1][h]), fmaxf(sM[2][h], sM[3][h]));
+        for (int e = tid; e < side * 8 * (D / 4); e += kThreads) {
+          const int hs = e / (8 * (D / 4)), h8 = e / (D / 4) % 8, d = (e % (D / 4)) * 4, h = nb * 8 + h8;
+          if (h >= live) continue;
+          const float top = top_of(hs, h);
           float L = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
+          for (int w = hs * deep; w < (hs + 1) * deep; ++w) {
             L += sL[w][h] * exp2f(sM[w][h] - top);
             const float2 x0 = *reinterpret_cast<const float2*>(join_buf + (w * 8 + h8) * T_::kPitch + d);
             const float2 x1 = *reinterpret_cast<const float2*>(join_buf + (w * 8 + h8) * T_::kPitch + d + 2);
@@ -574,14 +635,16 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
             o[3] += x1.y;
           }
           if (any_bad) L = NAN;
+          const int kvh = cc.kg * side + hs;
           if (whole) {
-            const float r = v_scale / L;
+            const float r = (TYPE == kTypeE4m3 ? __ldg(c.v_scale + kvh) : 1.0f) / L;
             const int64_t to = (static_cast<int64_t>(cc.b) * a.Hq + kvh * geo.heads_per + hb + h) * D + d;
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
                 make_uint2(pack16(o[0] * r, o[1] * r, a.q_type), pack16(o[2] * r, o[3] * r, a.q_type));
           } else {
-            *reinterpret_cast<float4*>(sp.o + (part * T_::kHeads + h) * D + d) = make_float4(o[0], o[1], o[2], o[3]);
-            if (d == 0) sp.ml[part * T_::kHeads + h] = make_float2(top, L);
+            const int64_t to = (part * side + hs) * T_::kHeads + h;
+            *reinterpret_cast<float4*>(sp.o + to * D + d) = make_float4(o[0], o[1], o[2], o[3]);
+            if (d == 0) sp.ml[to] = make_float2(top, L);
           }
         }
       }
@@ -592,73 +655,72 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   }
 }
 
-// The segments that cross runs: o = (sum over the runs, in order, of o_c 2^(m_c - m)) / l.
-// One CTA per (segment, head): kGroups groups of D / 4 threads take every kGroups-th run.
+// The segments that cross runs: o = (sum over the runs, in order, of o_c 2^(m_c - m)) / l. D / 4
+// threads take a head's dims, four each, and `teams` teams of as many share its pieces out.
 constexpr int kJoinThreads = 256;
 template <int D, int HEADS>
-__global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(PagedAttnArgs a, Geometry geo, Space sp) {
-  constexpr int kGroups = kJoinThreads / (D / 4);
-  __shared__ float4 sO[kGroups][D / 4];
-  __shared__ float sW[kJoinThreads / 32];
+__global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(PagedAttnArgs a, Geometry geo, Space sp, int teams) {
+  constexpr int kTeam = D / 4, kAhead = 8;
+  __shared__ float4 sO[kJoinThreads];
+  __shared__ float2 sML[kJoinThreads / kTeam];
+  const int tid = threadIdx.x, team = tid / kTeam, d = tid % kTeam * 4;
+  const int per = kJoinThreads / kTeam / teams;          // heads of a CTA
+  const int rows = geo.side * HEADS;                     // heads of a listed segment
+  const int64_t head = static_cast<int64_t>(blockIdx.x) * per + team / teams;
+  const int64_t listed = head / rows;
+  const int r = static_cast<int>(head % rows);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int HH = a.c.heads * geo.hgroups;
-  const int64_t b = blockIdx.x / HH;
-  const int hh = static_cast<int>(blockIdx.x % HH), h = blockIdx.y;
-  const int kvh = hh / geo.hgroups, hb = (hh % geo.hgroups) * HEADS;
-  if (hb + h >= geo.heads_per) return;
-  const int64_t before = sp.prefix[b], nblk = sp.prefix[b + 1] - before, units = sp.prefix[a.B] * HH;
-  const int64_t C = min(geo.ctas, units);
-  if (nblk == 0) return;
-  const int64_t s0 = before * HH + hh * nblk, s1 = s0 + nblk;
-  const int64_t c0 = unit_owner(s0, units, C), c1 = unit_owner(s1 - 1, units, C);
-  if (c0 == c1) return;  // finished by its run
-  const int pieces = static_cast<int>(c1 - c0 + 1);
-  const int tid = threadIdx.x;
-  auto at = [&](int p) {  // the segment begins in run c0 and goes on in the later ones
-    return (2 * (c0 + p) + (p > 0 ? 1 : 0)) * HEADS + h;
-  };
-  float top = kNoMax;
-  for (int p = tid; p < pieces; p += kJoinThreads) top = fmaxf(top, sp.ml[at(p)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  if (tid % 32 == 0) sW[tid / 32] = top;
-  __syncthreads();
-  for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, sW[w]);
-  const int grp = tid / (D / 4), d4 = tid % (D / 4);
+  const int4 job = listed < geo.listed ? sp.joins[listed] : make_int4(0, 0, 0, 0);
+  const int pieces = job.x, c0 = job.y;                  // no pieces: finished by its run
+  const int kvh = job.w / geo.hgroups * geo.side + r / HEADS, h = (job.w % geo.hgroups) * HEADS + r % HEADS;
+  const bool live = pieces > 0 && h < geo.heads_per;
+  float top = kNoMax, L = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float L = 0.0f;
-#pragma unroll 4
-  for (int p = grp; p < pieces; p += kGroups) {
-    const float2 ml = sp.ml[at(p)];
-    const float4 v = *reinterpret_cast<const float4*>(sp.o + static_cast<int64_t>(at(p)) * D + 4 * d4);
-    const float f = exp2f(ml.x - top);
-    L += ml.y * f;
-    o.x += v.x * f;
-    o.y += v.y * f;
-    o.z += v.z * f;
-    o.w += v.w * f;
-  }
-  sO[grp][d4] = o;
-  __shared__ float sL[kGroups];
-  if (d4 == 0) sL[grp] = L;
-  __syncthreads();
-  if (grp == 0) {
-    for (int k = 1; k < kGroups; ++k) {
-      const float4 v = sO[k][d4];
-      o.x += v.x;
-      o.y += v.y;
-      o.z += v.z;
-      o.w += v.w;
-      L += sL[k];
+  auto add = [&](float m, float l, float4 v) {
+    const float up = fmaxf(top, m), f = exp2f(top - up), fm = exp2f(m - up);
+    top = up;
+    L = L * f + l * fm;
+    o.x = o.x * f + v.x * fm;
+    o.y = o.y * f + v.y * fm;
+    o.z = o.z * f + v.z * fm;
+    o.w = o.w * f + v.w * fm;
+  };
+  if (live)
+    for (int p0 = team % teams; p0 < pieces; p0 += kAhead * teams) {
+      float2 ml[kAhead];
+      float4 v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int p = min(p0 + k * teams, pieces - 1);
+        const int64_t at = (2 * static_cast<int64_t>(c0 + p) + (p > 0 ? 1 : 0)) * rows + r;  // it begins in run c0 and goes on
+        ml[k] = sp.ml[at];
+        v[k] = *reinterpret_cast<const float4*>(sp.o + at * D + d);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (p0 + k * teams < pieces) add(ml[k].x, ml[k].y, v[k]);
     }
-    const float r = (a.c.type == kTypeE4m3 ? __ldg(a.c.v_scale + kvh) : 1.0f) / L;
-    const int64_t to = (b * a.Hq + kvh * geo.heads_per + hb + h) * D + 4 * d4;
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
-        make_uint2(pack16(o.x * r, o.y * r, a.q_type), pack16(o.z * r, o.w * r, a.q_type));
+  if (teams > 1) {
+    sO[tid] = o;
+    if (d == 0) sML[team] = make_float2(top, L);
+    __syncthreads();
+    if (team % teams) return;
+    for (int k = 1; k < teams; ++k) add(sML[team + k].x, sML[team + k].y, sO[tid + k * kTeam]);
   }
+  if (!live) return;
+  const float x = (a.c.type == kTypeE4m3 ? __ldg(a.c.v_scale + kvh) : 1.0f) / L;
+  const int64_t to = (static_cast<int64_t>(job.z) * a.Hq + kvh * geo.heads_per + h) * D + d;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
+      make_uint2(pack16(o.x * x, o.y * x, a.q_type), pack16(o.z * x, o.w * x, a.q_type));
 }
 
-constexpr int kMaxCtas = 3 * 148;  // three CTAs on each of a B200's SMs
+// Heads of a CTA: where the heads of a token lie side by side and a row is short, the four
+// warps take four heads of the same tokens instead of four runs of tokens of one head, so that
+// what is read at one time lies together.
+int heads_side_by_side(const PagedCache& c, int64_t segments) {
+  if (c.head_dim * type_bytes(c.type) > 128 || c.head_stride >= c.slot_stride || segments < kMaxCtas / 2) return 1;
+  return c.heads % 4 == 0 ? 4 : (c.heads % 2 == 0 ? 2 : 1);
+}
 
 int head_blocks(int Hq, int Hkv, int D) { return Hq / Hkv > 8 && D <= 128 ? 2 : 1; }
 
@@ -669,29 +731,37 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* lau
   geo.cap = static_cast<int>(std::min<int64_t>(a.c.max_pages * a.c.page_size, INT32_MAX - 1024));
   geo.heads_per = a.Hq / a.c.heads;
   geo.hgroups = static_cast<int>(ceil_div(geo.heads_per, T_::kHeads));
-  const int64_t segments = a.B * a.c.heads * geo.hgroups;
-  geo.ctas = std::min<int64_t>(std::min(kMaxCtas, T_::kCtas * num_sms), segments * ceil_div(geo.cap, T_::kUnit));
+  geo.side = heads_side_by_side(a.c, a.B * a.c.heads * geo.hgroups);
+  const int unit = T_::kTok * kWarps / geo.side;  // tokens of a unit
+  const int64_t segments = a.B * (a.c.heads / geo.side) * geo.hgroups;
+  geo.ctas = std::min<int64_t>(std::min(kMaxCtas, T_::kCtas * num_sms), segments * ceil_div(geo.cap, unit));
+  geo.by_segment = segments <= geo.ctas;
+  geo.listed = std::min(segments, geo.ctas);
   Space sp;
   sp.o = static_cast<float*>(a.workspace);
-  sp.ml = reinterpret_cast<float2*>(sp.o + 2 * kMaxCtas * T_::kHeads * D);
-  sp.prefix = reinterpret_cast<int64_t*>(sp.ml + 2 * kMaxCtas * T_::kHeads);
-  geo.block_pages = a.c.page_size % 16 == 0;
+  sp.ml = reinterpret_cast<float2*>(sp.o + 2 * kMaxCtas * geo.side * T_::kHeads * D);
+  sp.joins = reinterpret_cast<int4*>(sp.ml + 2 * kMaxCtas * geo.side * T_::kHeads);
   const int es = type_bytes(TYPE);
-  geo.page16 = static_cast<uint32_t>(a.c.page_stride * es / 16);
-  geo.slot16 = static_cast<uint32_t>(a.c.slot_stride * es / 16);
-  geo.head16 = static_cast<uint32_t>(a.c.head_stride * es / 16);
+  geo.page32 = static_cast<uint32_t>(a.c.page_stride * es / 32);
+  geo.slot32 = static_cast<uint32_t>(a.c.slot_stride * es / 32);
+  geo.head32 = static_cast<uint32_t>(a.c.head_stride * es / 32);
   // ceil(2^(31 + s) / page_size) with the least s of 2^s >= page_size is below 2^32 and exact
   geo.page_shift = 31;
   while ((int64_t(1) << (geo.page_shift - 31)) < a.c.page_size) ++geo.page_shift;
   geo.page_mul = static_cast<uint32_t>(((uint64_t(1) << geo.page_shift) + a.c.page_size - 1) / a.c.page_size);
-  paged_attn_kernel<D, TYPE, NB><<<static_cast<unsigned>(geo.ctas), kThreads, 0, s>>>(a, geo, sp);
+  const bool whole = a.c.page_size % 16 == 0;
+  auto kernel = whole ? paged_attn_kernel<D, TYPE, NB, true> : paged_attn_kernel<D, TYPE, NB, false>;
+  kernel<<<static_cast<unsigned>(geo.ctas), kThreads, 0, s>>>(a, geo, sp);
   *launches += 1;
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (geo.cap <= T_::kUnit) return cudaSuccess;  // a segment is one unit: none crosses runs
+  if (geo.cap <= unit) return cudaSuccess;  // a segment is one unit: none crosses runs
   // The join may be set up while the runs still work; it waits for them before it reads.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(segments), static_cast<unsigned>(std::min(T_::kHeads, geo.heads_per)));
+  // few segments have many pieces each: eight teams share a head's pieces out
+  const int64_t heads = geo.listed * geo.side * T_::kHeads;
+  const int teams = heads <= kMaxCtas ? std::min(8, kJoinThreads / (D / 4)) : 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(heads * teams, kJoinThreads / (D / 4))));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute early;
@@ -699,7 +769,7 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* lau
   early.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, T_::kHeads>, a, geo, sp);
+  e = cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, T_::kHeads>, a, geo, sp, teams);
   *launches += 1;
   return e;
 }
@@ -722,9 +792,9 @@ cudaError_t launch_d(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* l
 
 }  // namespace
 
-int64_t paged_attn_workspace(int64_t B, int Hq, int Hkv, int D) {
-  const int64_t heads = head_blocks(Hq, Hkv, D) * 8;
-  return 2 * kMaxCtas * heads * (D * 4 + 8) + (B + 1) * 8;
+int64_t paged_attn_workspace(int Hq, int Hkv, int D, int type) {
+  const int64_t heads = head_blocks(Hq, Hkv, D) * 8 * (D * type_bytes(type) <= 128 ? 4 : 1);
+  return 2 * kMaxCtas * heads * (D * 4 + 8) + kMaxCtas * 16;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* launches) {

@@ -106,8 +106,8 @@ CACHE = dict(k=P, v=P, dtype=2, num_pages=4, page_size=16, heads=2, head_dim=128
              seqs=3, max_pages=4, ts=4)
 BAD_CACHES = ((dict(k=0), 1), (dict(v=0), 1), (dict(table=0), 1), (dict(dtype=1), 1), (dict(dtype=3), 1), (dict(head_dim=80), 2),
               (dict(heads=0), 2), (dict(page_size=0), 2), (dict(num_pages=0), 2), (dict(seqs=0), 2), (dict(max_pages=0), 2),
-              (dict(max_pages=1 << 30), 2), (dict(k=P + 8), 1), (dict(ps=4097), 1), (dict(ss=4), 1), (dict(hs=-128), 1),
-              (dict(table=P + 2), 1), (dict(num_pages=1 << 31), 2), (dict(ps=1 << 34), 2), (dict(ps=1 << 62), 2))
+              (dict(max_pages=1 << 30), 2), (dict(k=P + 16), 1), (dict(ps=4097), 1), (dict(ss=8), 1), (dict(hs=-128), 1),
+              (dict(table=P + 2), 1), (dict(num_pages=1 << 31), 2), (dict(ps=1 << 35), 2), (dict(ps=1 << 62), 2))
 
 
 def _cache(**kw):
@@ -149,8 +149,8 @@ def test_paged_attention_refusals():
                    (dict(ws=P + 4), 1), (dict(len=P + 2), 1), (dict(qh=-128), 1), (dict(c=NULL), 1)):
         assert _attention(**kw) == st, kw
     lib = awq.library()
-    assert lib.awq_paged_attention_workspace(3, 4, 2, 128) > 0
-    for bad in ((0, 4, 2, 128), (3, 5, 2, 128), (3, 4, 0, 128), (3, 4, 2, 80)):
+    assert lib.awq_paged_attention_workspace(4, 2, 128, 2) > 0
+    for bad in ((5, 2, 128, 2), (4, 0, 128, 2), (4, 2, 80, 2), (4, 2, 128, 1)):
         assert lib.awq_paged_attention_workspace(*bad) == 0
 
 
