@@ -9,6 +9,8 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <utility>
+
 #include "awq_kernels.h"
 
 namespace awq {
@@ -90,6 +92,29 @@ bool decode_device_memory(const void* p, int dev);  // memory of device `dev`, o
 void record_launch_count(int launches);
 
 #ifdef __CUDACC__
+// Programmatic launches: a kernel is set up while the one before it in the stream still works,
+// and waits for that one's end, with all it has written, before it touches memory. Every CTA
+// waits, so that a kernel's end implies the end of all before it.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, int* launches,
+                         Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  if (e == cudaSuccess) *launches += 1;
+  return e;
+}
+
 __device__ __forceinline__ float bits_f16(uint32_t h) { return __half2float(__ushort_as_half(static_cast<unsigned short>(h))); }
 // The two 16-bit values of a word as floats.
 __device__ __forceinline__ float2 unpack16(uint32_t w, int type) {
@@ -137,6 +162,24 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int type, const float
                    pack16(v[6], v[7], type));
   }
 }
+// Eight consecutive values (16-byte aligned) as floats.
+__device__ __forceinline__ void load8(const void* p, int64_t i, int type, float (&v)[8]) {
+  if (type == kTypeF32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = s[0], b = s[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack16(u[k], type);
+      v[2 * k] = f.x;
+      v[2 * k + 1] = f.y;
+    }
+  }
+}
 // Eight consecutive 16- or 32-bit values (16-byte aligned) in their own form, read once.
 template <int BYTES>
 struct Raw8 {
@@ -144,7 +187,10 @@ struct Raw8 {
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * BYTES);
 #pragma unroll
-    for (int k = 0; k < BYTES / 2; ++k) w[k] = s[k];
+    for (int k = 0; k < BYTES / 2; ++k)
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w)
+                   : "l"(s + k));
   }
   __device__ __forceinline__ void to_float(float (&v)[8], int type) const {
     if constexpr (BYTES == 4) {

@@ -38,6 +38,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 3 * 148;  // three CTAs on each of a B200's SMs
+constexpr int kWhole = 4;           // units of the longest segment that is not cut
 
 template <int D, int TYPE, int NB>
 struct Tile {
@@ -93,15 +94,15 @@ struct Piece {
   uint32_t w[BYTES / 4];
   __device__ __forceinline__ void load(const uint8_t* p) {
     if constexpr (BYTES == 32)
-      asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                    : "l"(p));
     else if constexpr (BYTES == 16)
-      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                    : "l"(p));
     else
-      asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+      asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -124,7 +125,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 // A sequence's tokens as the kernel takes them: never more than its table row can name.
 __device__ __forceinline__ int clamped_length(const int32_t* lengths, int64_t b, int cap) {
-  return min(max(__ldg(lengths + b), 0), cap);
+  return min(max(lengths[b], 0), cap);
 }
 
 // The run of CTA c when T units are dealt to C CTAs, and the CTA whose run holds unit l.
@@ -177,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   __shared__ float sM[kWarps][T_::kHeads], sL[kWarps][T_::kHeads];
   __shared__ int sBad[kWarps];
   __shared__ int64_t sScan[kWarps + 1];
+  __shared__ int sSnap[2];  // units from the run's even ends to those of segments
   __shared__ Cursor sStart;
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t = lane & 3;
@@ -185,55 +187,79 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   const int HH = c.heads / side * geo.hgroups;
   const int deep = kWarps / side, head_of = warp / deep, tok_of = warp % deep * kTok;  // the warp's head and tokens of a unit
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join is set up meanwhile
+  wait_for_previous();
+  start_next();  // the join is set up meanwhile
 
-  // ---- the run: exclusive sums of the sequences' units, then the sequence of its first unit
+  // ---- the run: exclusive sums of the sequences' units, then the places of its two ends
   const int64_t per = ceil_div(a.B, kThreads), b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
   int64_t mine = 0;
-  for (int64_t b = b0; b < b1; ++b) mine += (clamped_length(a.lengths, b, geo.cap) + unit - 1) / unit;
+  int longest = 0;
+  for (int64_t b = b0; b < b1; ++b) {
+    const int nblk = (clamped_length(a.lengths, b, geo.cap) + unit - 1) / unit;
+    mine += nblk;
+    longest = max(longest, nblk);
+  }
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t up = __shfl_up_sync(~0u, incl, o);
     if (lane >= o) incl += up;
   }
-  if (lane == 31) sScan[warp] = incl;
+  longest = __reduce_max_sync(~0u, longest);
+  if (lane == 31) {
+    sScan[warp] = incl;
+    sBad[warp] = longest;
+  }
+  if (tid < 2) sSnap[tid] = 0;
   __syncthreads();
   int64_t before = incl - mine, total = 0;
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += sScan[w];
     total += sScan[w];
+    longest = max(longest, sBad[w]);
   }
-  // no run is empty: with fewer units than CTAs the later CTAs have none
+  // No run is empty: with fewer units than CTAs the later CTAs have none. Where segments are short a
+  // run begins and ends with one instead (and may be empty): a join takes longer than kWhole units.
   const int64_t units = total * HH, C = min(geo.ctas, units);
-  const int64_t u0 = blockIdx.x < C ? run_start(blockIdx.x, units, C) : 0;
-  const int n = blockIdx.x < C ? static_cast<int>(run_start(blockIdx.x + 1, units, C) - u0) : 0;
-  if (n > 0 && before * HH <= u0 && u0 < (before + mine) * HH) {
-    int64_t at = before * HH;
-    for (int64_t b = b0; b < b1; ++b) {
-      const int len = clamped_length(a.lengths, b, geo.cap), nblk = (len + unit - 1) / unit;
-      if (u0 < at + static_cast<int64_t>(nblk) * HH) {
-        const int64_t rel = u0 - at;
-        const int hh = static_cast<int>(rel / nblk);
-        sStart = {static_cast<int>(b), hh / geo.hgroups, hh % geo.hgroups, static_cast<int>(rel % nblk), len};
-        break;
+  const bool snap = longest <= kWhole;
+  int64_t ends_at[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    ends_at[e] = blockIdx.x < C ? run_start(blockIdx.x + e, units, C) : 0;
+    const int64_t u = ends_at[e];
+    if (before * HH <= u && u < (before + mine) * HH) {
+      int64_t at = before * HH;
+      for (int64_t b = b0; b < b1; ++b) {
+        const int len = clamped_length(a.lengths, b, geo.cap), nblk = (len + unit - 1) / unit;
+        if (u < at + static_cast<int64_t>(nblk) * HH) {
+          const int64_t rel = u - at;
+          int hh = static_cast<int>(rel / nblk), blk = static_cast<int>(rel % nblk);
+          if (snap && blk > 0) {
+            sSnap[e] = nblk - blk;
+            blk = nblk - 1;  // the unit before the run: it goes on from there
+          }
+          if (e == 0) sStart = {static_cast<int>(b), hh / geo.hgroups, hh % geo.hgroups, blk, len};
+          break;
+        }
+        at += static_cast<int64_t>(nblk) * HH;
       }
-      at += static_cast<int64_t>(nblk) * HH;
     }
   }
   // sequences without tokens have no units: their rows of zeros are dealt out too
   for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x)
-    if (__ldg(a.lengths + b) <= 0) {
+    if (a.lengths[b] <= 0) {
       if (geo.by_segment)
         for (int i = tid; i < HH; i += kThreads) sp.joins[b * HH + i] = make_int4(0, 0, 0, 0);
       for (int64_t i = tid; i < static_cast<int64_t>(a.Hq) * D / 2; i += kThreads)
         static_cast<uint32_t*>(a.out)[b * a.Hq * D / 2 + i] = 0u;
     }
-  if (n == 0) {
+  __syncthreads();
+  const int64_t u0 = ends_at[0] + sSnap[0];
+  const int n = static_cast<int>(ends_at[1] + sSnap[1] - u0);
+  if (n <= 0) {
     if (tid == 0 && !geo.by_segment) sp.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
-  __syncthreads();
 
   auto advance = [&](Cursor& k) {
     if (++k.blk * unit < k.len) return;
@@ -251,7 +277,9 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   // ---- the loading side. look_up() asks the block table for a tile's pages one tile before
   // place() turns them into places of the cache, in units of 32 bytes: per block of 16 tokens
   // that of its first row if WHOLE, of row lane % 16 otherwise.
-  Cursor ic = sStart;
+  Cursor first = sStart;
+  if (sSnap[0] > 0) advance(first);
+  Cursor ic = first;
   int looked = 0;
   int32_t page[TB];            // asked for
   uint32_t within[TB];         // places from the page's to the row's
@@ -276,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
       const uint32_t pi = static_cast<uint32_t>(static_cast<uint64_t>(tok) * geo.page_mul >> geo.page_shift);
       within[k] = (tok - pi * c.page_size) * geo.slot32 + (ic.kg * side + head_of) * geo.head32;
       page[k] = -1;
-      if (16 * k + own < ask_rows) page[k] = __ldg(table + pi);
+      if (16 * k + own < ask_rows) page[k] = table[pi];
     }
   };
   auto place = [&]() {
@@ -364,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   look_up();
 
   // ---- the computing side
-  Cursor cc = sStart;
+  Cursor cc = first;
   uint32_t qf[NB][S][2];          // Q^T fragments: heads g of each block, this lane's dims
   float acc[NB][S][4];            // O^T: per 16-dim tile, (dim, dim + 1) x (heads 2t, 2t + 1)
   float ls[NB][2];                // l of heads 2t, 2t + 1
@@ -373,9 +401,9 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   for (int i = 0; i < n; ++i) {
     if (fresh) {  // a segment of the run begins
       fresh = false;
-      bad = __ldg(a.lengths + cc.b) > geo.cap;
+      bad = a.lengths[cc.b] > geo.cap;
       const int kvh = cc.kg * side + head_of, hb = cc.hg * T_::kHeads;
-      const float k_scale = TYPE == kTypeE4m3 ? __ldg(c.k_scale + kvh) : 1.0f;
+      const float k_scale = TYPE == kTypeE4m3 ? c.k_scale[kvh] : 1.0f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int h = hb + nb * 8 + g;
@@ -388,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
           // dims of step st: 4 elements of the lane's piece st / PER
           constexpr int PER = KB / (4 * ES);  // steps that a piece serves
           const int d = (st / PER) * (4 * KB / ES) + (KB / ES) * t + 4 * (st % PER);
-          const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(q + d)) : make_uint2(0u, 0u);
+          const uint2 w = live ? *reinterpret_cast<const uint2*>(q + d) : make_uint2(0u, 0u);
           qf[nb][st][0] = w.x ^ flip;
           qf[nb][st][1] = w.y ^ flip;
         }
@@ -637,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
           if (any_bad) L = NAN;
           const int kvh = cc.kg * side + hs;
           if (whole) {
-            const float r = (TYPE == kTypeE4m3 ? __ldg(c.v_scale + kvh) : 1.0f) / L;
+            const float r = (TYPE == kTypeE4m3 ? c.v_scale[kvh] : 1.0f) / L;
             const int64_t to = (static_cast<int64_t>(cc.b) * a.Hq + kvh * geo.heads_per + hb + h) * D + d;
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
                 make_uint2(pack16(o[0] * r, o[1] * r, a.q_type), pack16(o[2] * r, o[3] * r, a.q_type));
@@ -669,7 +697,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(PagedAttn
   const int64_t head = static_cast<int64_t>(blockIdx.x) * per + team / teams;
   const int64_t listed = head / rows;
   const int r = static_cast<int>(head % rows);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous();
+  start_next();
   const int4 job = listed < geo.listed ? sp.joins[listed] : make_int4(0, 0, 0, 0);
   const int pieces = job.x, c0 = job.y;                  // no pieces: finished by its run
   const int kvh = job.w / geo.hgroups * geo.side + r / HEADS, h = (job.w % geo.hgroups) * HEADS + r % HEADS;
@@ -708,7 +737,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(PagedAttn
     for (int k = 1; k < teams; ++k) add(sML[team + k].x, sML[team + k].y, sO[tid + k * kTeam]);
   }
   if (!live) return;
-  const float x = (a.c.type == kTypeE4m3 ? __ldg(a.c.v_scale + kvh) : 1.0f) / L;
+  const float x = (a.c.type == kTypeE4m3 ? a.c.v_scale[kvh] : 1.0f) / L;
   const int64_t to = (static_cast<int64_t>(job.z) * a.Hq + kvh * geo.heads_per + h) * D + d;
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
       make_uint2(pack16(o.x * x, o.y * x, a.q_type), pack16(o.z * x, o.w * x, a.q_type));
@@ -751,27 +780,14 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* lau
   geo.page_mul = static_cast<uint32_t>(((uint64_t(1) << geo.page_shift) + a.c.page_size - 1) / a.c.page_size);
   const bool whole = a.c.page_size % 16 == 0;
   auto kernel = whole ? paged_attn_kernel<D, TYPE, NB, true> : paged_attn_kernel<D, TYPE, NB, false>;
-  kernel<<<static_cast<unsigned>(geo.ctas), kThreads, 0, s>>>(a, geo, sp);
-  *launches += 1;
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_early(kernel, dim3(static_cast<unsigned>(geo.ctas)), kThreads, 0, s, launches, a, geo, sp);
   if (e != cudaSuccess) return e;
-  if (geo.cap <= unit) return cudaSuccess;  // a segment is one unit: none crosses runs
-  // The join may be set up while the runs still work; it waits for them before it reads.
-  cudaLaunchConfig_t cfg = {};
+  if (geo.cap <= kWhole * unit) return cudaSuccess;  // no segment crosses runs
   // few segments have many pieces each: eight teams share a head's pieces out
   const int64_t heads = geo.listed * geo.side * T_::kHeads;
   const int teams = heads <= kMaxCtas ? std::min(8, kJoinThreads / (D / 4)) : 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(heads * teams, kJoinThreads / (D / 4))));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, T_::kHeads>, a, geo, sp, teams);
-  *launches += 1;
-  return e;
+  const dim3 grid(static_cast<unsigned>(ceil_div(heads * teams, kJoinThreads / (D / 4))));
+  return launch_early(paged_attn_join_kernel<D, T_::kHeads>, grid, kJoinThreads, 0, s, launches, a, geo, sp, teams);
 }
 
 template <int D>

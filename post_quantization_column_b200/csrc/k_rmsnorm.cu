@@ -53,11 +53,89 @@ __device__ __forceinline__ float row_scale(uint32_t peak, float factor) {
   return scale == 0.0f ? 1.0f : scale;
 }
 
+// Rows of aligned vectors of 8 values: the whole row lies in the registers of its threads, 8
+// values per vector, between the reduction and the output. A row belongs to a warp (WARP, 8
+// rows a block) or to a block; several blocks an SM load while others reduce, and the weight
+// stays in the L1 cache, which the rows themselves pass by.
+constexpr int norm_threads(bool warp) { return warp ? 256 : 512; }  // of a block, at most
+constexpr int norm_blocks(int vpt, bool warp) { return (warp ? 2 : 1) * (vpt == 1 ? 3 : (vpt == 2 ? 2 : 1)); }  // of that size an SM
+template <int XB, int RB, int VPT, bool WARP>
+__global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) norm_kernel(NormArgs a) {
+  __shared__ RowStat parts[16];
+  const int lane = WARP ? threadIdx.x % 32 : threadIdx.x, width = WARP ? 32 : blockDim.x;
+  const int rows = WARP ? blockDim.x / 32 : 1;
+  const int vecs = static_cast<int>(a.K / 8);
+  wait_for_previous();
+  start_next();
+  for (int64_t m = static_cast<int64_t>(blockIdx.x) * rows + (WARP ? threadIdx.x / 32 : 0); m < a.M;
+       m += static_cast<int64_t>(gridDim.x) * rows) {
+    float h[VPT][8];
+    Raw8<XB> rx[VPT];
+    Raw8<RB == 0 ? 2 : RB> rr[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = lane + i * width;
+      if (v < vecs) {
+        rx[i].load(a.X, m * a.x_stride + 8 * v);
+        if (RB) rr[i].load(a.residual, m * a.r_stride + 8 * v);
+      }
+    }
+    RowStat st{0.0f, 0u};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = lane + i * width;
+      if (v >= vecs) continue;
+      rx[i].to_float(h[i], a.x_type);
+      if (RB) {
+        float r[8];
+        rr[i].to_float(r, a.r_type);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[i][k] = __fadd_rn(h[i][k], r[k]);
+        store8(a.residual_out, m * a.ro_stride + 8 * v, a.r_type, h[i]);
+      }
+      float w[8];
+      load8(a.weight, 8 * v, a.w_type, w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        st.ss = __fadd_rn(st.ss, __fmul_rn(h[i][k], h[i][k]));
+        h[i][k] = __fmul_rn(h[i][k], w[k]);
+        st.peak = max(st.peak, __float_as_uint(h[i][k]) & 0x7FFFFFFFu);
+      }
+    }
+    if (WARP) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        st = join(st, {__shfl_xor_sync(~0u, st.ss, o), __shfl_xor_sync(~0u, st.peak, o)});
+    } else {
+      st = block_join(st, parts);
+    }
+    const float factor = row_factor(st.ss, a.K, a.eps);
+    float scale = 1.0f;
+    if (a.out_type == kTypeE4m3) {
+      scale = row_scale(st.peak, factor);
+      if (lane == 0) a.out_scales[m] = scale;
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = lane + i * width;
+      if (v >= vecs) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        h[i][k] = __fmul_rn(h[i][k], factor);
+        if (a.out_type == kTypeE4m3) h[i][k] = __fdiv_rn(h[i][k], scale);
+      }
+      store8(a.out, m * a.K + 8 * v, a.out_type, h[i]);
+    }
+  }
+}
+
 // One row per block and turn, one or more scalars per thread: any K, stride and alignment.
 // h stays in shared memory between the two uses of it.
 __global__ void __launch_bounds__(1024) norm_any_kernel(NormArgs a) {
   extern __shared__ float h_row[];
   __shared__ RowStat parts[32];
+  wait_for_previous();
+  start_next();
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     RowStat st{0.0f, 0u};
     for (int64_t k = threadIdx.x; k < a.K; k += blockDim.x) {
@@ -83,16 +161,58 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(NormArgs a) {
 
 }  // namespace
 
+namespace {
+
+template <int XB, int RB, int VPT, bool WARP>
+cudaError_t launch_norm(const NormArgs& a, int threads, int num_sms, cudaStream_t s, int* launches) {
+  const int64_t per = WARP ? threads / 32 : 1;
+  const int resident = std::min(32, norm_threads(WARP) * norm_blocks(VPT, WARP) / threads);  // blocks an SM
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ceil_div(a.M, per), static_cast<int64_t>(resident) * num_sms));
+  return launch_early(norm_kernel<XB, RB, VPT, WARP>, dim3(blocks), threads, 0, s, launches, a);
+}
+
+template <int XB, int RB>
+cudaError_t launch_norm_types(const NormArgs& a, int num_sms, cudaStream_t s, int* launches) {
+  const int64_t vecs = a.K / 8;
+  if (vecs <= 128 && a.M > num_sms) {  // a warp per row
+    if (vecs <= 32) return launch_norm<XB, RB, 1, true>(a, 256, num_sms, s, launches);
+    if (vecs <= 64) return launch_norm<XB, RB, 2, true>(a, 256, num_sms, s, launches);
+    return launch_norm<XB, RB, 4, true>(a, 256, num_sms, s, launches);
+  }
+  const int vpt = vecs <= 512 ? 1 : (vecs <= 1024 ? 2 : 4);
+  const int threads = static_cast<int>(ceil_div(ceil_div(vecs, vpt), 32) * 32);
+  if (vpt == 1) return launch_norm<XB, RB, 1, false>(a, threads, num_sms, s, launches);
+  if (vpt == 2) return launch_norm<XB, RB, 2, false>(a, threads, num_sms, s, launches);
+  return launch_norm<XB, RB, 4, false>(a, threads, num_sms, s, launches);
+}
+
+bool rows_aligned(const void* p, int64_t stride, int type) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride * type_bytes(type) % 16 == 0;
+}
+
+}  // namespace
+
 cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s, int* launches) {
+  // the vector form: 16-byte vectors everywhere (8 bytes of an e4m3 output) and a row in registers
+  if (a.K % 8 == 0 && a.K <= 16384 && rows_aligned(a.X, a.x_stride, a.x_type) && rows_aligned(a.weight, 0, a.w_type) &&
+      (a.out_type == kTypeE4m3 ? (reinterpret_cast<uintptr_t>(a.out) & 7u) == 0 : rows_aligned(a.out, a.K, a.out_type)) &&
+      (!a.residual || (rows_aligned(a.residual, a.r_stride, a.r_type) && rows_aligned(a.residual_out, a.ro_stride, a.r_type)))) {
+    const int xb = type_bytes(a.x_type), rb = a.residual ? type_bytes(a.r_type) : 0;
+    if (xb == 2) {
+      if (rb == 0) return launch_norm_types<2, 0>(a, num_sms, s, launches);
+      if (rb == 2) return launch_norm_types<2, 2>(a, num_sms, s, launches);
+      return launch_norm_types<2, 4>(a, num_sms, s, launches);
+    }
+    if (rb == 0) return launch_norm_types<4, 0>(a, num_sms, s, launches);
+    if (rb == 2) return launch_norm_types<4, 2>(a, num_sms, s, launches);
+    return launch_norm_types<4, 4>(a, num_sms, s, launches);
+  }
   const int threads = static_cast<int>(std::min<int64_t>(1024, ceil_div(a.K, 32) * 32));
-  const size_t smem = static_cast<size_t>(a.K) * 4;
   static unsigned long long done = 0;
-  cudaError_t e = set_smem_limit_once(norm_any_kernel, static_cast<int>(kNormMaxK * 4), &done);
+  const cudaError_t e = set_smem_limit_once(norm_any_kernel, static_cast<int>(kNormMaxK * 4), &done);
   if (e != cudaSuccess) return e;
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(a.M, 8 * num_sms));
-  norm_any_kernel<<<blocks, threads, smem, s>>>(a);
-  *launches += 1;
-  return cudaGetLastError();
+  return launch_early(norm_any_kernel, dim3(blocks), threads, static_cast<size_t>(a.K) * 4, s, launches, a);
 }
 
 }  // namespace awq
