@@ -14,7 +14,6 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-import struct
 from dataclasses import dataclass
 
 import torch
@@ -676,47 +675,46 @@ def qdq_in_loss_gemm(M: int, K: int, N: int, n_grid: int = 20, group: int = 128,
 
 
 # ---- the other operators of a decode step ------------------------------------------------
-# They are called between every two products of a decode step, so their argument marshalling
-# is kept short: plain integers to the C ABI, the raw handle of the current stream.
+# Their arguments are marshalled by _decode.so, a CPython module: they are called between every two
+# products of a decode step, where ctypes took longer than their kernels.
 
-_DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2, torch.float8_e4m3fn: 3}
-_HALVES = (torch.float16, torch.bfloat16)
-_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
-_PAGED_CACHE = struct.Struct("@16q")   # awq_paged_cache: pointers and 64-bit sizes
+_decode_module = None
 
 
-def _on_device(device, tensors):
-    """The tensors (None among them) lie on the CUDA device `device` and carry no gradient."""
-    for t in tensors:
-        if t is not None:
-            if t.device != device:
-                raise ValueError(f"every tensor must be on {device}, got one on {t.device}")
-            if t.requires_grad and torch.is_grad_enabled():
-                raise ValueError("the decode-step operators have no backward pass: call them under torch.no_grad()")
+def _load_decode():
+    """The compiled binding _decode.so (raises if it has not been built)."""
+    global _decode_module
+    if _decode_module is None:
+        library()
+        try:
+            from . import _decode as module
+        except ImportError as e:
+            raise RuntimeError(f"_decode.so is missing or does not load ({e}): build it with "
+                               "`python -m post_quantization_column_b200.build`") from e
+        _decode_module = module
+    return _decode_module
 
 
-def _launch_stream(stream, device, tensors) -> int:
-    """Handle of the stream a call runs on (default: the current stream of `device`). Another
-    stream first waits for the current one, and the caching allocator is told of the tensors."""
-    raw = torch._C._cuda_getCurrentRawStream(device.index)
-    if stream is None or stream.cuda_stream == raw:
-        return raw
-    if stream.device != device:
-        raise ValueError(f"the stream must be one of {device}")
-    stream.wait_stream(torch.cuda.current_stream(device))
-    for t in tensors:
-        if t is not None and t.numel():
+def _on_stream(stream, call, args):
+    """call(*args) on `stream`, which first waits for the current stream; the caching allocator is
+    told which tensors are used on which stream."""
+    device = stream.device
+    current = torch.cuda.current_stream(device)
+    tensors = [t for t in args if isinstance(t, torch.Tensor) and t.is_cuda]
+    if any(t.device != device for t in tensors):
+        raise ValueError("the stream must be one of the tensors' device")
+    if stream == current:
+        return call(*args)
+    stream.wait_stream(current)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    if out.__class__ is not int:   # a status: nothing was enqueued
+        for t in tensors:
             t.record_stream(stream)
-    return stream.cuda_stream
-
-
-def _status_ptr(status, device) -> int:
-    if status is None:
-        return 0
-    if status.dtype != torch.int32 or status.numel() != 1 or not (status.device == device or
-                                                                  (not status.is_cuda and status.is_pinned())):
-        raise ValueError("status must be one int32 on the device or in pinned host memory")
-    return status.data_ptr()
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(current)
+    return out
 
 
 def check_status(status: torch.Tensor) -> None:
@@ -738,46 +736,12 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residu
     Returns y (M, K) in ``out_dtype`` (fp16, bf16 or fp32), or for torch.float8_e4m3fn
     ``(codes, scales)``: codes = e4m3(y / scales), one fp32 scale max|y| / 448 per row.
     Asynchronous on `stream`."""
-    device = X.device
-    if not X.is_cuda:
-        raise ValueError("rms_norm() takes CUDA tensors")
-    if X.dim() != 2 or weight.shape != (X.shape[1],):
-        raise ValueError("X must be (M, K) and weight (K,)")
-    if X.dtype not in _FLOATS or weight.dtype not in _FLOATS:
-        raise TypeError("X and weight must be float32, float16 or bfloat16")
-    out_code = _DTYPES.get(out_dtype)
-    if out_code is None:
-        raise TypeError("out_dtype must be float32, float16, bfloat16 or float8_e4m3fn")
-    M, K = X.shape
-    _on_device(device, (X, weight, residual, residual_out))
-    if X.stride(1) != 1:
-        X = X.contiguous()
-    weight = weight.contiguous()
-    r_ptr = r_code = r_stride = ro_ptr = ro_stride = 0
-    if residual is not None:
-        if residual_out is None:
-            residual_out = residual
-        if residual.shape != X.shape or residual.dtype not in _FLOATS:
-            raise ValueError("residual must be (M, K) in float32, float16 or bfloat16")
-        if residual_out.shape != X.shape or residual_out.dtype != residual.dtype or (K > 1 and residual_out.stride(1) != 1):
-            raise ValueError("residual_out must be (M, K) of the residual's dtype with contiguous rows")
-        if residual.stride(1) != 1:
-            residual = residual.contiguous()
-        r_ptr, r_code, r_stride = residual.data_ptr(), _DTYPES[residual.dtype], residual.stride(0)
-        ro_ptr, ro_stride = residual_out.data_ptr(), residual_out.stride(0) if M > 1 else K
-        if M == 1:
-            r_stride = K
-    elif residual_out is not None:
-        raise ValueError("residual_out comes with a residual")
-    out = torch.empty(M, K, dtype=out_dtype, device=device)
-    scales = torch.empty(M, dtype=torch.float32, device=device) if out_code == 3 else None
-    raw = _launch_stream(stream, device, (X, weight, residual, residual_out, out, scales))
-    st = library().awq_rms_norm(X.data_ptr(), _DTYPES[X.dtype], X.stride(0), r_ptr, r_code, r_stride, ro_ptr, ro_stride,
-                                weight.data_ptr(), _DTYPES[weight.dtype], M, K, eps, out.data_ptr(), out_code,
-                                0 if scales is None else scales.data_ptr(), raw)
-    if st:
-        _check(st)
-    return out if scales is None else (out, scales)
+    args = (X, weight, eps, residual, residual_out, out_dtype)
+    call = (_decode_module or _load_decode()).rms_norm
+    out = call(*args) if stream is None else _on_stream(stream, call, args)
+    if out.__class__ is int:
+        _check(out)
+    return out
 
 
 ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
@@ -803,46 +767,6 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | N
     return freqs.to(dev), magnitude.value
 
 
-def _cache_args(k_cache, v_cache, block_table, k_scale, v_scale, n_seqs):
-    """awq_paged_cache of the caches (num_pages, page_size, heads, head_dim), in any memory
-    order with contiguous rows, and the block table (n_seqs, max_pages)."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must be (num_pages, page_size, heads, head_dim) of one dtype")
-    stride = k_cache.stride()
-    if stride[3] != 1 or v_cache.stride() != stride:
-        raise ValueError("k_cache and v_cache must have contiguous rows and the same strides")
-    code = _DTYPES.get(k_cache.dtype, 1)
-    if code == 1:
-        raise TypeError("the cache must be float16, bfloat16 or float8_e4m3fn")
-    pages, page_size, heads, head_dim = k_cache.shape
-    ks = vs = 0
-    if code == 3:
-        for s in (k_scale, v_scale):
-            if s is None or s.dtype != torch.float32 or s.shape != (heads,) or not s.is_contiguous():
-                raise ValueError("an e4m3 cache needs k_scale and v_scale, (heads,) contiguous float32")
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("k_scale and v_scale belong to an e4m3 cache")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1 and block_table.shape[1] > 1:
-        raise ValueError("block_table must be (sequences, max_pages) int32 with contiguous rows")
-    seqs, max_pages = block_table.shape
-    if n_seqs is not None and n_seqs != seqs:
-        raise ValueError("block_table needs one row per sequence")
-    return _PAGED_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), code, pages, page_size, heads, head_dim, *stride[:3],
-                             ks, vs, block_table.data_ptr(), seqs, max_pages, block_table.stride(0)), heads, head_dim
-
-
-def _rows16(t, name, heads, head_dim):
-    """(T, heads, head_dim) with 16-byte aligned contiguous rows: as it is, or a copy."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
-        raise ValueError(f"{name} must be (tokens, heads, head_dim) = (T, {heads}, {head_dim})")
-    st, sh, sd = t.stride()
-    per = 16 // t.element_size()
-    if sd != 1 or st % per or sh % per or t.data_ptr() % 16:
-        t = t.clone(memory_format=torch.contiguous_format)
-    return t
-
-
 def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
               block_table: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor | None = None, *,
               seqs: torch.Tensor | None = None, interleaved: bool = False, magnitude: float = 1.0,
@@ -854,53 +778,18 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache:
 
     q (T, Hq, D), k and v (T, heads, D): fp32, fp16 or bf16, e.g. views of one QKV product;
     caches (num_pages, page_size, heads, D): fp16, bf16 or e4m3 with ``k_scale`` / ``v_scale``
-    (heads,); ``block_table`` (sequences, max_pages) int32; ``positions`` (T,) int32, negative for
-    padded rows (zero queries, nothing appended); ``seqs`` (T,) int32 is each token's sequence
-    (None: token t is sequence t's, as in decode); ``freqs`` (rotary_dim / 2,) float64 from
-    rope_frequencies, None for no rotation. ``q_dtype`` (default: the cache's, fp16 for e4m3).
-    Tokens outside the table or the cache are not appended and set ``status`` (check_status).
-    Two tokens must not name one place of the cache. Asynchronous on `stream`."""
-    device = k.device
-    if not k.is_cuda:
-        raise ValueError("kv_append() takes CUDA tensors")
-    _on_device(device, (q, k, v, k_cache, v_cache, block_table, positions, freqs, seqs, k_scale, v_scale))
-    cache, heads, head_dim = _cache_args(k_cache, v_cache, block_table, k_scale, v_scale, None)
-    T = k.shape[0]
-    k, v = _rows16(k, "k", heads, head_dim), _rows16(v, "v", heads, head_dim)
-    if v.shape[0] != T or v.dtype != k.dtype or k.dtype not in _FLOATS:
-        raise ValueError("q, k and v must share T and a dtype of float32, float16 or bfloat16")
-    if q_dtype is None:
-        q_dtype = torch.float16 if k_cache.dtype == torch.float8_e4m3fn else k_cache.dtype
-    if q_dtype not in _HALVES:
-        raise TypeError("q_dtype must be float16 or bfloat16")
-    Hq = q_ptr = q_st = q_sh = out_ptr = 0
-    out = None
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be (T, Hq, head_dim)")
-        Hq = q.shape[1]
-        q = _rows16(q, "q", Hq, head_dim)
-        if q.shape[0] != T or q.dtype != k.dtype:
-            raise ValueError("q, k and v must share T and a dtype of float32, float16 or bfloat16")
-        out = torch.empty(T, Hq, head_dim, dtype=q_dtype, device=device)
-        q_ptr, out_ptr, (q_st, q_sh, _) = q.data_ptr(), out.data_ptr(), q.stride()
-    for t in (positions, seqs):
-        if t is not None and (t.dtype != torch.int32 or t.shape != (T,) or not t.is_contiguous()):
-            raise ValueError("positions and seqs must be (T,) contiguous int32")
-    rot = f_ptr = 0
-    if freqs is not None:
-        if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
-            raise ValueError("freqs must be a contiguous float64 vector (rope_frequencies)")
-        rot, f_ptr = 2 * freqs.shape[0], freqs.data_ptr()
-    st_ptr = _status_ptr(status, device)
-    raw = _launch_stream(stream, device, (q, k, v, k_cache, v_cache, block_table, positions, freqs, seqs, k_scale, v_scale, out))
-    k_st, k_sh, _ = k.stride()
-    v_st, v_sh, _ = v.stride()
-    st = library().awq_kv_append(q_ptr, q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(), v_st, v_sh, _DTYPES[k.dtype], T, Hq,
-                                 out_ptr, _DTYPES[q_dtype], positions.data_ptr(), 0 if seqs is None else seqs.data_ptr(),
-                                 f_ptr, rot, interleaved, magnitude, cache, st_ptr, raw)
-    if st:
-        _check(st)
+    (heads,), rows 32-byte aligned; ``block_table`` (sequences, max_pages) int32; ``positions``
+    (T,) int32, negative for padded rows (zero queries, nothing appended); ``seqs`` (T,) int32 is
+    each token's sequence (None: token t is sequence t's, as in decode); ``freqs``
+    (rotary_dim / 2,) float64 from rope_frequencies, None for no rotation; ``q_dtype`` (default:
+    the cache's, fp16 for e4m3). Tokens outside the table or the cache are not appended and set
+    ``status`` (check_status). Two tokens must not name one place of the cache. Asynchronous on
+    `stream`."""
+    args = (q, k, v, k_cache, v_cache, block_table, positions, freqs, seqs, interleaved, magnitude, k_scale, v_scale, q_dtype, status)
+    call = (_decode_module or _load_decode()).kv_append
+    out = call(*args) if stream is None else _on_stream(stream, call, args)
+    if out.__class__ is int:
+        _check(out)
     return out
 
 
@@ -914,32 +803,9 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     kv_append's, ``lengths`` (sequences,) int32 (0 or less: a row of zeros), ``scale`` default
     1 / sqrt(D). Returns (sequences, Hq, D) in q's dtype. A sequence whose length or pages lie
     outside the table or the cache gives NaN and sets ``status``. Asynchronous on `stream`."""
-    device = q.device
-    if not q.is_cuda:
-        raise ValueError("paged_attention() takes CUDA tensors")
-    _on_device(device, (q, k_cache, v_cache, block_table, lengths, k_scale, v_scale))
-    if q.dim() != 3 or q.dtype not in _HALVES:
-        raise ValueError("q must be (sequences, Hq, head_dim) float16 or bfloat16")
-    B, Hq, D = q.shape
-    if B == 0:
-        return torch.empty_like(q)
-    cache, heads, head_dim = _cache_args(k_cache, v_cache, block_table, k_scale, v_scale, B)
-    if D != head_dim or Hq % heads:
-        raise ValueError("q's head_dim must be the cache's, and the cache's heads must divide q's")
-    if k_cache.dtype != q.dtype and k_cache.dtype != torch.float8_e4m3fn:
-        raise TypeError("a 16-bit cache and its queries share a dtype")
-    if lengths.dtype != torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous():
-        raise ValueError("lengths must be (sequences,) contiguous int32")
-    q = _rows16(q, "q", Hq, D)
-    lib = library()
-    size = lib.awq_paged_attention_workspace(Hq, heads, D, _DTYPES[k_cache.dtype])
-    out = torch.empty(B, Hq, D, dtype=q.dtype, device=device)
-    ws = torch.empty(size, dtype=torch.uint8, device=device)
-    st_ptr = _status_ptr(status, device)
-    raw = _launch_stream(stream, device, (q, k_cache, v_cache, block_table, lengths, k_scale, v_scale, out, ws))
-    q_sb, q_sh, _ = q.stride()
-    st = lib.awq_paged_attention(q.data_ptr(), q_sb, q_sh, _DTYPES[q.dtype], Hq, cache, lengths.data_ptr(),
-                                 D ** -0.5 if scale is None else scale, out.data_ptr(), ws.data_ptr(), size, st_ptr, raw)
-    if st:
-        _check(st)
+    args = (q, k_cache, v_cache, block_table, lengths, scale, k_scale, v_scale, status)
+    call = (_decode_module or _load_decode()).paged_attention
+    out = call(*args) if stream is None else _on_stream(stream, call, args)
+    if out.__class__ is int:
+        _check(out)
     return out

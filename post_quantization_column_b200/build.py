@@ -2,6 +2,8 @@
 
     python -m post_quantization_column_b200.build [--force] [--verbose]
 
+and _decode.so, the CPython binding of the decode-step operators, with the C++ compiler.
+
 Objects go to ``post_quantization_column_b200/_build/`` (not committed); the shared
 library is written next to this file so the package finds it without installation.
 """
@@ -18,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libawqsearch.so")
+BINDING = os.path.join(PKG, "_decode.so")
 SOURCES = ["awq_api.cu", "k_statistic.cu", "k_qdq.cu", "k_loss_gemm.cu", "k_clip.cu", "k_w4a16.cu", "k_module.cu", "k_attn.cu", "awq_noalloc.cu", "gemm_policy.cu",
            "awq_decode.cu", "k_rmsnorm.cu", "k_kv_append.cu", "k_paged_attn.cu"]
 HEADERS = ["awq_device.cuh", "awq_kernels.h", "qdq_tile.cuh", "decode_kernels.h"]
@@ -73,7 +76,32 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
+    build_binding(force, verbose)
     return LIB
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/decode_binding.cpp against torch's headers and link it to the library next to it."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "decode_binding.cpp")
+    if not (force or _stale(BINDING, [src, os.path.join(ROOT, "include", "awq_search.h")])):
+        return BINDING
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler found; it is required to build _decode.so")
+    t = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", src, "-o", BINDING, f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", os.path.join(t, "include"), "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           "-L", PKG, "-lawqsearch", "-L", os.path.join(t, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    return BINDING
 
 
 def main(argv=None) -> int:

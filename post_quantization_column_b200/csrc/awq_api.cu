@@ -610,8 +610,17 @@ int decode_error(int status, const char* msg) {
 }
 int decode_cuda_error(cudaError_t e, const char* where) { return cuda_error(e, where); }
 int decode_device(const void* ptr, int* dev, int* num_sms) {
-  bind_device(nullptr, ptr);
-  return check_device(dev, num_sms);
+  static int sms[64];  // of the devices that have been checked
+  if (*dev < 0)
+    bind_device(nullptr, ptr);
+  else
+    cudaSetDevice(*dev);
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return cuda_error(e, "cudaGetDevice");
+  if (*dev < 64 && (*num_sms = __atomic_load_n(&sms[*dev], __ATOMIC_RELAXED)) > 0) return AWQ_OK;
+  const int st = check_device(dev, num_sms);
+  if (st == AWQ_OK && *dev < 64) __atomic_store_n(&sms[*dev], *num_sms, __ATOMIC_RELAXED);
+  return st;
 }
 bool decode_device_memory(const void* p, int dev) {
   cudaPointerAttributes at;

@@ -25,8 +25,14 @@ bool ranges_meet(const void* a, int64_t sa, int64_t wa, const void* b, int64_t s
   return a0 < b0 + (rows - 1) * sb + wb && b0 < a0 + (rows - 1) * sa + wa;
 }
 
-// The memory of a call's pointers lies on the device it runs on.
-int check_memory(const void* const* ptrs, int n, int dev) {
+constexpr int kAsk = -1;  // the device of the call is asked of its pointers
+
+// Makes the device of the call current: the caller's, which owns all its pointers (the Python
+// binding knows its tensors' device), or that of `first`, where every pointer must lie.
+int take_device(int device, const void* first, const void* const* ptrs, int n, int* num_sms) {
+  int dev = device;
+  const int st = decode_device(first, &dev, num_sms);
+  if (st != AWQ_OK || device != kAsk) return st;
   for (int i = 0; i < n; ++i)
     if (ptrs[i] && !decode_device_memory(ptrs[i], dev))
       return decode_error(AWQ_ERR_INVALID_ARG, "inputs and outputs must be memory of the device the call runs on");
@@ -89,7 +95,7 @@ int take_cache(const awq_paged_cache* in, PagedCache* out) {
 
 extern "C" {
 
-int awq_rms_norm(const void* X, int x_dtype, int64_t x_stride, const void* residual, int r_dtype, int64_t r_stride,
+int awq_rms_norm_on(int device, const void* X, int x_dtype, int64_t x_stride, const void* residual, int r_dtype, int64_t r_stride,
                  void* residual_out, int64_t ro_stride, const void* weight, int w_dtype, int64_t M, int64_t K,
                  float eps, void* out, int out_dtype, float* out_scales, awq_stream_t stream) {
   decode_error(AWQ_OK, "");
@@ -119,10 +125,10 @@ int awq_rms_norm(const void* X, int x_dtype, int64_t x_stride, const void* resid
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DeviceRestore restore_device;
-  int dev = 0, num_sms = 0, st = decode_device(X, &dev, &num_sms);
-  if (st != AWQ_OK) return st;
   const void* ptrs[] = {X, residual, residual_out, weight, out, out_dtype == kTypeE4m3 ? out_scales : nullptr};
-  if ((st = check_memory(ptrs, 6, dev)) != AWQ_OK) return st;
+  int num_sms = 0;
+  const int st = take_device(device, X, ptrs, 6, &num_sms);
+  if (st != AWQ_OK) return st;
   NormArgs a;
   a.X = X;
   a.residual = residual;
@@ -145,6 +151,11 @@ int awq_rms_norm(const void* X, int x_dtype, int64_t x_stride, const void* resid
   if (e != cudaSuccess) return decode_cuda_error(e, "RMS norm");
   record_launch_count(launches);
   return AWQ_OK;
+}
+int awq_rms_norm(const void* X, int x_dtype, int64_t x_stride, const void* residual, int r_dtype, int64_t r_stride,
+                 void* residual_out, int64_t ro_stride, const void* weight, int w_dtype, int64_t M, int64_t K,
+                 float eps, void* out, int out_dtype, float* out_scales, awq_stream_t stream) {
+  return awq_rms_norm_on(kAsk, X, x_dtype, x_stride, residual, r_dtype, r_stride, residual_out, ro_stride, weight, w_dtype, M, K, eps, out, out_dtype, out_scales, stream);
 }
 
 int awq_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double original_len, double low,
@@ -182,7 +193,7 @@ int awq_rope_frequencies(int rotary_dim, double base, int scaling, double factor
   return AWQ_OK;
 }
 
-int awq_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
+int awq_kv_append_on(int device, const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
                   int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride, int in_dtype,
                   int64_t T, int Hq, void* q_out, int q_dtype, const int32_t* positions, const int32_t* seqs,
                   const double* freqs, int rotary_dim, int interleaved, float magnitude, const awq_paged_cache* cache,
@@ -218,11 +229,10 @@ int awq_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, 
     return decode_error(AWQ_ERR_INVALID_ARG, "positions, seqs, freqs or status is misaligned");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DeviceRestore restore_device;
-  int dev = 0, num_sms = 0;
-  if ((st = decode_device(k, &dev, &num_sms)) != AWQ_OK) return st;
   const void* ptrs[] = {k, v, positions, a.c.k, a.c.v, a.c.table, Hq > 0 ? q : nullptr, Hq > 0 ? q_out : nullptr, seqs,
                         rotary_dim > 0 ? freqs : nullptr, a.c.k_scale, a.c.v_scale};
-  if ((st = check_memory(ptrs, 12, dev)) != AWQ_OK) return st;
+  int num_sms = 0;
+  if ((st = take_device(device, k, ptrs, 12, &num_sms)) != AWQ_OK) return st;
   a.q = q;
   a.k = k;
   a.v = v;
@@ -250,6 +260,13 @@ int awq_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, 
   record_launch_count(launches);
   return AWQ_OK;
 }
+int awq_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                  int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride, int in_dtype,
+                  int64_t T, int Hq, void* q_out, int q_dtype, const int32_t* positions, const int32_t* seqs,
+                  const double* freqs, int rotary_dim, int interleaved, float magnitude, const awq_paged_cache* cache,
+                  int32_t* status, awq_stream_t stream) {
+  return awq_kv_append_on(kAsk, q, q_token_stride, q_head_stride, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, in_dtype, T, Hq, q_out, q_dtype, positions, seqs, freqs, rotary_dim, interleaved, magnitude, cache, status, stream);
+}
 
 int64_t awq_paged_attention_workspace(int Hq, int Hkv, int head_dim, int cache_dtype) {
   if (Hkv < 1 || Hq < Hkv || Hq % Hkv || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
@@ -258,7 +275,7 @@ int64_t awq_paged_attention_workspace(int Hq, int Hkv, int head_dim, int cache_d
   return paged_attn_workspace(Hq, Hkv, head_dim, cache_dtype);
 }
 
-int awq_paged_attention(const void* q, int64_t q_seq_stride, int64_t q_head_stride, int q_dtype, int Hq,
+int awq_paged_attention_on(int device, const void* q, int64_t q_seq_stride, int64_t q_head_stride, int q_dtype, int Hq,
                         const awq_paged_cache* cache, const int32_t* lengths, float scale, void* out, void* workspace,
                         int64_t workspace_bytes, int32_t* status, awq_stream_t stream) {
   decode_error(AWQ_OK, "");
@@ -281,10 +298,9 @@ int awq_paged_attention(const void* q, int64_t q_seq_stride, int64_t q_head_stri
     return decode_error(AWQ_ERR_INVALID_ARG, "the work space is smaller than awq_paged_attention_workspace says");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DeviceRestore restore_device;
-  int dev = 0, num_sms = 0;
-  if ((st = decode_device(q, &dev, &num_sms)) != AWQ_OK) return st;
   const void* ptrs[] = {q, a.c.k, a.c.v, a.c.table, lengths, out, workspace, a.c.k_scale, a.c.v_scale};
-  if ((st = check_memory(ptrs, 9, dev)) != AWQ_OK) return st;
+  int num_sms = 0;
+  if ((st = take_device(device, q, ptrs, 9, &num_sms)) != AWQ_OK) return st;
   a.q = q;
   a.q_sb = q_seq_stride;
   a.q_sh = q_head_stride;
@@ -301,6 +317,11 @@ int awq_paged_attention(const void* q, int64_t q_seq_stride, int64_t q_head_stri
   if (e != cudaSuccess) return decode_cuda_error(e, "paged attention");
   record_launch_count(launches);
   return AWQ_OK;
+}
+int awq_paged_attention(const void* q, int64_t q_seq_stride, int64_t q_head_stride, int q_dtype, int Hq,
+                        const awq_paged_cache* cache, const int32_t* lengths, float scale, void* out, void* workspace,
+                        int64_t workspace_bytes, int32_t* status, awq_stream_t stream) {
+  return awq_paged_attention_on(kAsk, q, q_seq_stride, q_head_stride, q_dtype, Hq, cache, lengths, scale, out, workspace, workspace_bytes, status, stream);
 }
 
 }  // extern "C"

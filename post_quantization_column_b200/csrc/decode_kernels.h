@@ -86,7 +86,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int num_sms, cudaStream_t 
 // Shared with awq_api.cu: the entry points' error text, device selection and launch count.
 int decode_error(int status, const char* msg);
 int decode_cuda_error(cudaError_t e, const char* where);
-// Makes the device that owns `ptr` current and checks it.
+// Makes device *dev current, or for -1 the device that owns `ptr`, and checks it once.
 int decode_device(const void* ptr, int* dev, int* num_sms);
 bool decode_device_memory(const void* p, int dev);  // memory of device `dev`, or managed memory
 void record_launch_count(int launches);

@@ -1,6 +1,7 @@
 """Pins of the decode-step operators' oracle, and their library's host side (CPU only)."""
 import ctypes
 import math
+import struct
 
 import numpy as np
 import pytest
@@ -111,7 +112,7 @@ BAD_CACHES = ((dict(k=0), 1), (dict(v=0), 1), (dict(table=0), 1), (dict(dtype=1)
 
 
 def _cache(**kw):
-    return awq._PAGED_CACHE.pack(*{**CACHE, **kw}.values())
+    return struct.pack("@16q", *{**CACHE, **kw}.values())   # awq_paged_cache
 
 
 def _append(cache=None, **kw):
