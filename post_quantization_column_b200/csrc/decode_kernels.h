@@ -147,61 +147,52 @@ __device__ __forceinline__ void store_one(void* p, int64_t i, int type, float v)
   }
 }
 // Eight consecutive values (16-byte aligned; 8 bytes for e4m3) rounded to `type`.
-__device__ __forceinline__ void store8(void* p, int64_t i, int type, const float (&v)[8]) {
-  if (type == kTypeF32) {
+template <int TYPE>
+__device__ __forceinline__ void store8_as(void* p, int64_t i, const float (&v)[8]) {
+  if constexpr (TYPE == kTypeF32) {
     float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
     d[0] = make_float4(v[0], v[1], v[2], v[3]);
     d[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else if (type == kTypeE4m3) {
+  } else if constexpr (TYPE == kTypeE4m3) {
     const uint32_t lo = pack_e4m3(v[0], v[1]) | (pack_e4m3(v[2], v[3]) << 16);
     const uint32_t hi = pack_e4m3(v[4], v[5]) | (pack_e4m3(v[6], v[7]) << 16);
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + i) = make_uint2(lo, hi);
   } else {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-        make_uint4(pack16(v[0], v[1], type), pack16(v[2], v[3], type), pack16(v[4], v[5], type),
-                   pack16(v[6], v[7], type));
+        make_uint4(pack16(v[0], v[1], TYPE), pack16(v[2], v[3], TYPE), pack16(v[4], v[5], TYPE), pack16(v[6], v[7], TYPE));
   }
 }
-// Eight consecutive values (16-byte aligned) as floats.
-__device__ __forceinline__ void load8(const void* p, int64_t i, int type, float (&v)[8]) {
-  if (type == kTypeF32) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = s[0], b = s[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack16(u[k], type);
-      v[2 * k] = f.x;
-      v[2 * k + 1] = f.y;
-    }
+__device__ __forceinline__ void store8(void* p, int64_t i, int type, const float (&v)[8]) {
+  switch (type) {
+    case kTypeF32: store8_as<kTypeF32>(p, i, v); break;
+    case kTypeBf16: store8_as<kTypeBf16>(p, i, v); break;
+    case kTypeF16: store8_as<kTypeF16>(p, i, v); break;
+    default: store8_as<kTypeE4m3>(p, i, v);
   }
 }
-// Eight consecutive 16- or 32-bit values (16-byte aligned) in their own form, read once.
-template <int BYTES>
+// Eight consecutive values (16-byte aligned) in their own form, read once.
+template <int TYPE>
 struct Raw8 {
-  uint4 w[BYTES / 2];
+  static constexpr int kWords = TYPE == kTypeF32 ? 2 : 1;
+  uint4 w[kWords];
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * BYTES);
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * type_bytes(TYPE));
 #pragma unroll
-    for (int k = 0; k < BYTES / 2; ++k)
+    for (int k = 0; k < kWords; ++k)
       asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w)
                    : "l"(s + k));
   }
-  __device__ __forceinline__ void to_float(float (&v)[8], int type) const {
-    if constexpr (BYTES == 4) {
-      const uint4 a = w[0], b = w[BYTES / 2 - 1];
+  __device__ __forceinline__ void to_float(float (&v)[8]) const {
+    if constexpr (TYPE == kTypeF32) {
+      const uint4 a = w[0], b = w[kWords - 1];
       v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
       v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
     } else {
       const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 f = unpack16(u[k], type);
+        const float2 f = unpack16(u[k], TYPE);
         v[2 * k] = f.x;
         v[2 * k + 1] = f.y;
       }

@@ -33,40 +33,39 @@ __device__ __forceinline__ void unit_dims(int u, int rot, bool half_pairs, int* 
 
 // One token per blockIdx.x; each of the gridDim.y blocks of the token takes U units per thread
 // of its Hq + 2 Hkv heads, and has them on the way before it works out the angles.
-template <int XB, int U>
+template <int IN, int CACHE, int U>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a) {
-  __shared__ float sCos[kMaxRot / 2], sSin[kMaxRot / 2];
+  __shared__ __align__(16) float sCos[kMaxRot / 2], sSin[kMaxRot / 2];
   const int64_t t = blockIdx.x;
   const PagedCache& c = a.c;
   const int D = c.head_dim, shift = 31 - __clz(D / 16);  // log2 of a head's units
   const int units = (a.Hq + 2 * c.heads) << shift;
   wait_for_previous();
   start_next();
-  Raw8<XB> r0[U], r1[U];
+  const int64_t q_at = t * a.q_st, k_at = t * a.k_st, v_at = t * a.v_st;
+  Raw8<IN> r0[U], r1[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int w = (blockIdx.y * U + i) * kAppendThreads + threadIdx.x;
     if (w >= units) continue;
-    const int head = w >> shift, u = w & ((1 << shift) - 1);
-    const bool is_q = head < a.Hq, is_v = head >= a.Hq + c.heads;
+    const int head = w >> shift, u = w & ((1 << shift) - 1), kh = head - a.Hq, vh = kh - c.heads;
     int d0, d1;
-    unit_dims(u, a.rot, !is_v && !a.interleaved, &d0, &d1);
-    const void* src = is_q ? a.q : (is_v ? a.v : a.k);
-    const int64_t at = is_q ? t * a.q_st + head * a.q_sh
-                            : (is_v ? t * a.v_st + (head - a.Hq - c.heads) * a.v_sh : t * a.k_st + (head - a.Hq) * a.k_sh);
+    unit_dims(u, a.rot, vh < 0 && !a.interleaved, &d0, &d1);
+    const void* src = kh < 0 ? a.q : (vh < 0 ? a.k : a.v);
+    const int64_t at = kh < 0 ? q_at + head * a.q_sh : (vh < 0 ? k_at + kh * a.k_sh : v_at + vh * a.v_sh);
     r0[i].load(src, at + d0);
     r1[i].load(src, at + d1);
   }
   const int pos = a.positions[t];
   const int64_t seq = a.seq ? a.seq[t] : t;
   const int half = a.rot / 2;
-  for (int i = threadIdx.x; i < half; i += kAppendThreads) {
-    const double turns = static_cast<double>(pos) * a.freqs[i] * 0.15915494309189533577;  // 1 / (2 pi)
+  if (threadIdx.x < half) {  // rot <= 256: one angle per thread
+    const double turns = static_cast<double>(pos) * a.freqs[threadIdx.x] * 0.15915494309189533577;  // 1 / (2 pi)
     const float frac = static_cast<float>(turns - rint(turns));
     float sn, cs;
     sincospif(2.0f * frac, &sn, &cs);
-    sCos[i] = __fmul_rn(a.magnitude, cs);
-    sSin[i] = __fmul_rn(a.magnitude, sn);
+    sCos[threadIdx.x] = __fmul_rn(a.magnitude, cs);
+    sSin[threadIdx.x] = __fmul_rn(a.magnitude, sn);
   }
   // where the token's keys and values go
   int64_t row = -1;
@@ -84,74 +83,97 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a)
   for (int i = 0; i < U; ++i) {
     const int w = (blockIdx.y * U + i) * kAppendThreads + threadIdx.x;
     if (w >= units) continue;
-    const int head = w >> shift, u = w & ((1 << shift) - 1);
-    const bool is_q = head < a.Hq, is_v = head >= a.Hq + c.heads;
-    if (!is_q && row < 0) continue;
-    const int hh = is_q ? head : (is_v ? head - a.Hq - c.heads : head - a.Hq);
+    const int head = w >> shift, u = w & ((1 << shift) - 1), kh = head - a.Hq, vh = kh - c.heads;
     int d0, d1;
-    unit_dims(u, a.rot, !is_v && !a.interleaved, &d0, &d1);
+    unit_dims(u, a.rot, vh < 0 && !a.interleaved, &d0, &d1);
     float x[8], y[8];
-    r0[i].to_float(x, a.in_type);
-    r1[i].to_float(y, a.in_type);
-    if (!is_v && 16 * u < a.rot) {
+    r0[i].to_float(x);
+    r1[i].to_float(y);
+    if (vh < 0 && 16 * u < a.rot) {
+      float cs[8], sn[8];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        *reinterpret_cast<float4*>(cs + 4 * k) = *reinterpret_cast<const float4*>(sCos + 8 * u + 4 * k);
+        *reinterpret_cast<float4*>(sn + 4 * k) = *reinterpret_cast<const float4*>(sSin + 8 * u + 4 * k);
+      }
       if (a.interleaved) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float c0 = sCos[8 * u + k], s0 = sSin[8 * u + k], c1 = sCos[8 * u + 4 + k], s1 = sSin[8 * u + 4 + k];
           const float xa = x[2 * k], xb = x[2 * k + 1], ya = y[2 * k], yb = y[2 * k + 1];
-          x[2 * k] = xa * c0 - xb * s0;
-          x[2 * k + 1] = xa * s0 + xb * c0;
-          y[2 * k] = ya * c1 - yb * s1;
-          y[2 * k + 1] = ya * s1 + yb * c1;
+          x[2 * k] = xa * cs[k] - xb * sn[k];
+          x[2 * k + 1] = xa * sn[k] + xb * cs[k];
+          y[2 * k] = ya * cs[4 + k] - yb * sn[4 + k];
+          y[2 * k + 1] = ya * sn[4 + k] + yb * cs[4 + k];
         }
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float cs = sCos[8 * u + k], sn = sSin[8 * u + k], xa = x[k], xb = y[k];
-          x[k] = xa * cs - xb * sn;
-          y[k] = xa * sn + xb * cs;
+          const float xa = x[k], xb = y[k];
+          x[k] = xa * cs[k] - xb * sn[k];
+          y[k] = xa * sn[k] + xb * cs[k];
         }
       }
     }
-    if (is_q) {
-      const int64_t to = (t * a.Hq + hh) * D;
+    if (kh < 0) {
+      const int64_t to = (t * a.Hq + head) * D;
       if (pos < 0) {  // a padded row of the batch
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = y[k] = 0.0f;
       }
-      store8(a.q_out, to + d0, a.q_type, x);
-      store8(a.q_out, to + d1, a.q_type, y);
-    } else {
-      if (c.type == kTypeE4m3) {
-        const float scale = (is_v ? c.v_scale : c.k_scale)[hh];
+      if (a.q_type == kTypeBf16) {
+        store8_as<kTypeBf16>(a.q_out, to + d0, x);
+        store8_as<kTypeBf16>(a.q_out, to + d1, y);
+      } else {
+        store8_as<kTypeF16>(a.q_out, to + d0, x);
+        store8_as<kTypeF16>(a.q_out, to + d1, y);
+      }
+    } else if (row >= 0) {
+      const int hh = vh < 0 ? kh : vh;
+      if constexpr (CACHE == kTypeE4m3) {
+        const float scale = (vh < 0 ? c.k_scale : c.v_scale)[hh];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           x[k] = __fdiv_rn(x[k], scale);
           y[k] = __fdiv_rn(y[k], scale);
         }
       }
-      void* dst = is_v ? c.v : c.k;
-      store8(dst, row + hh * c.head_stride + d0, c.type, x);
-      store8(dst, row + hh * c.head_stride + d1, c.type, y);
+      void* dst = vh < 0 ? c.k : c.v;
+      const int64_t to = row + hh * c.head_stride;
+      store8_as<CACHE>(dst, to + d0, x);
+      store8_as<CACHE>(dst, to + d1, y);
     }
   }
 }
 
-template <int XB>
+template <int IN, int CACHE>
 cudaError_t launch(const AppendArgs& a, int num_sms, cudaStream_t s, int* launches) {
   const int units = (a.Hq + 2 * a.c.heads) * (a.c.head_dim / 16);
   const int64_t blocks = ceil_div(units, kAppendThreads);  // of a token, at one unit per thread
   // a few tokens are spread over the SMs; of many each block takes what it can keep on the way
   const int per = a.T * blocks < 4 * num_sms || blocks == 1 ? 1 : (blocks == 2 || blocks == 4 ? 2 : 3);
   const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>(ceil_div(blocks, per)));
-  auto kernel = per == 1 ? kv_append_kernel<XB, 1> : (per == 2 ? kv_append_kernel<XB, 2> : kv_append_kernel<XB, 3>);
+  auto kernel = per == 1 ? kv_append_kernel<IN, CACHE, 1>
+                         : (per == 2 ? kv_append_kernel<IN, CACHE, 2> : kv_append_kernel<IN, CACHE, 3>);
   return launch_early(kernel, grid, kAppendThreads, 0, s, launches, a);
+}
+
+template <int IN>
+cudaError_t launch_cache(const AppendArgs& a, int num_sms, cudaStream_t s, int* launches) {
+  switch (a.c.type) {
+    case kTypeBf16: return launch<IN, kTypeBf16>(a, num_sms, s, launches);
+    case kTypeF16: return launch<IN, kTypeF16>(a, num_sms, s, launches);
+    default: return launch<IN, kTypeE4m3>(a, num_sms, s, launches);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendArgs& a, int num_sms, cudaStream_t s, int* launches) {
-  return type_bytes(a.in_type) == 4 ? launch<4>(a, num_sms, s, launches) : launch<2>(a, num_sms, s, launches);
+  switch (a.in_type) {
+    case kTypeF32: return launch_cache<kTypeF32>(a, num_sms, s, launches);
+    case kTypeF16: return launch_cache<kTypeF16>(a, num_sms, s, launches);
+    default: return launch_cache<kTypeBf16>(a, num_sms, s, launches);
+  }
 }
 
 }  // namespace awq

@@ -53,53 +53,70 @@ __device__ __forceinline__ float row_scale(uint32_t peak, float factor) {
   return scale == 0.0f ? 1.0f : scale;
 }
 
-// Rows of aligned vectors of 8 values: the whole row lies in the registers of its threads, 8
-// values per vector, between the reduction and the output. A row belongs to a warp (WARP, 8
-// rows a block) or to a block; several blocks an SM load while others reduce, and the weight
-// stays in the L1 cache, which the rows themselves pass by.
+// Rows of aligned vectors of 8 values: the whole row lies in the registers of its threads, VPT
+// vectors each, between the reduction and the output. A row belongs to a warp (WARP, 8 rows a
+// block) or to a block; several blocks an SM load while others reduce, and the weight stays in
+// the L1 cache, which the rows themselves pass by.
 constexpr int norm_threads(bool warp) { return warp ? 256 : 512; }  // of a block, at most
 constexpr int norm_blocks(int vpt, bool warp) { return (warp ? 2 : 1) * (vpt == 1 ? 3 : (vpt == 2 ? 2 : 1)); }  // of that size an SM
-template <int XB, int RB, int VPT, bool WARP>
+template <int TX, int TR, int VPT, bool WARP>
 __global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) norm_kernel(NormArgs a) {
   __shared__ RowStat parts[16];
   const int lane = WARP ? threadIdx.x % 32 : threadIdx.x, width = WARP ? 32 : blockDim.x;
   const int rows = WARP ? blockDim.x / 32 : 1;
   const int vecs = static_cast<int>(a.K / 8);
+  const bool codes = a.out_type == kTypeE4m3;
   wait_for_previous();
   start_next();
   for (int64_t m = static_cast<int64_t>(blockIdx.x) * rows + (WARP ? threadIdx.x / 32 : 0); m < a.M;
        m += static_cast<int64_t>(gridDim.x) * rows) {
-    float h[VPT][8];
-    Raw8<XB> rx[VPT];
-    Raw8<RB == 0 ? 2 : RB> rr[VPT];
+    Raw8<TX> rx[VPT];
+    Raw8<TR == kTypeNone ? kTypeF16 : TR> rr[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = lane + i * width;
       if (v < vecs) {
         rx[i].load(a.X, m * a.x_stride + 8 * v);
-        if (RB) rr[i].load(a.residual, m * a.r_stride + 8 * v);
+        if (TR != kTypeNone) rr[i].load(a.residual, m * a.r_stride + 8 * v);
       }
     }
+    float h[VPT][8];
     RowStat st{0.0f, 0u};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = lane + i * width;
       if (v >= vecs) continue;
-      rx[i].to_float(h[i], a.x_type);
-      if (RB) {
+      rx[i].to_float(h[i]);
+      if constexpr (TR != kTypeNone) {
         float r[8];
-        rr[i].to_float(r, a.r_type);
+        rr[i].to_float(r);
 #pragma unroll
         for (int k = 0; k < 8; ++k) h[i][k] = __fadd_rn(h[i][k], r[k]);
-        store8(a.residual_out, m * a.ro_stride + 8 * v, a.r_type, h[i]);
+        store8_as<TR>(a.residual_out, m * a.ro_stride + 8 * v, h[i]);
       }
-      float w[8];
-      load8(a.weight, 8 * v, a.w_type, w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        st.ss = __fadd_rn(st.ss, __fmul_rn(h[i][k], h[i][k]));
-        h[i][k] = __fmul_rn(h[i][k], w[k]);
-        st.peak = max(st.peak, __float_as_uint(h[i][k]) & 0x7FFFFFFFu);
+      for (int k = 0; k < 8; ++k) st.ss = __fmaf_rn(h[i][k], h[i][k], st.ss);
+      float w[8];
+      if (a.w_type == kTypeF32) {
+        const float4* from = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + 8 * v);
+        const float4 lo = from[0], hi = from[1];
+        w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
+        w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
+      } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + 8 * v);
+        const uint32_t words[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = unpack16(words[k], a.w_type);
+          w[2 * k] = f.x;
+          w[2 * k + 1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[i][k] = __fmul_rn(h[i][k], w[k]);
+      if (codes) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) st.peak = max(st.peak, __float_as_uint(h[i][k]) & 0x7FFFFFFFu);
       }
     }
     if (WARP) {
@@ -110,21 +127,26 @@ __global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) no
       st = block_join(st, parts);
     }
     const float factor = row_factor(st.ss, a.K, a.eps);
-    float scale = 1.0f;
-    if (a.out_type == kTypeE4m3) {
-      scale = row_scale(st.peak, factor);
+    if (codes) {
+      const float scale = row_scale(st.peak, factor);
       if (lane == 0) a.out_scales[m] = scale;
-    }
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = lane + i * width;
-      if (v >= vecs) continue;
+      for (int i = 0; i < VPT; ++i) {
+        const int v = lane + i * width;
+        if (v >= vecs) continue;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        h[i][k] = __fmul_rn(h[i][k], factor);
-        if (a.out_type == kTypeE4m3) h[i][k] = __fdiv_rn(h[i][k], scale);
+        for (int k = 0; k < 8; ++k) h[i][k] = __fdiv_rn(__fmul_rn(h[i][k], factor), scale);
+        store8_as<kTypeE4m3>(a.out, m * a.K + 8 * v, h[i]);
       }
-      store8(a.out, m * a.K + 8 * v, a.out_type, h[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = lane + i * width;
+        if (v >= vecs) continue;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[i][k] = __fmul_rn(h[i][k], factor);
+        store8(a.out, m * a.K + 8 * v, a.out_type, h[i]);
+      }
     }
   }
 }
@@ -163,27 +185,36 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(NormArgs a) {
 
 namespace {
 
-template <int XB, int RB, int VPT, bool WARP>
+template <int TX, int TR, int VPT, bool WARP>
 cudaError_t launch_norm(const NormArgs& a, int threads, int num_sms, cudaStream_t s, int* launches) {
   const int64_t per = WARP ? threads / 32 : 1;
   const int resident = std::min(32, norm_threads(WARP) * norm_blocks(VPT, WARP) / threads);  // blocks an SM
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ceil_div(a.M, per), static_cast<int64_t>(resident) * num_sms));
-  return launch_early(norm_kernel<XB, RB, VPT, WARP>, dim3(blocks), threads, 0, s, launches, a);
+  return launch_early(norm_kernel<TX, TR, VPT, WARP>, dim3(blocks), threads, 0, s, launches, a);
 }
 
-template <int XB, int RB>
+template <int TX, int TR>
 cudaError_t launch_norm_types(const NormArgs& a, int num_sms, cudaStream_t s, int* launches) {
   const int64_t vecs = a.K / 8;
   if (vecs <= 128 && a.M > num_sms) {  // a warp per row
-    if (vecs <= 32) return launch_norm<XB, RB, 1, true>(a, 256, num_sms, s, launches);
-    if (vecs <= 64) return launch_norm<XB, RB, 2, true>(a, 256, num_sms, s, launches);
-    return launch_norm<XB, RB, 4, true>(a, 256, num_sms, s, launches);
+    if (vecs <= 32) return launch_norm<TX, TR, 1, true>(a, 256, num_sms, s, launches);
+    return launch_norm<TX, TR, 4, true>(a, 256, num_sms, s, launches);
   }
   const int vpt = vecs <= 512 ? 1 : (vecs <= 1024 ? 2 : 4);
   const int threads = static_cast<int>(ceil_div(ceil_div(vecs, vpt), 32) * 32);
-  if (vpt == 1) return launch_norm<XB, RB, 1, false>(a, threads, num_sms, s, launches);
-  if (vpt == 2) return launch_norm<XB, RB, 2, false>(a, threads, num_sms, s, launches);
-  return launch_norm<XB, RB, 4, false>(a, threads, num_sms, s, launches);
+  if (vpt == 1) return launch_norm<TX, TR, 1, false>(a, threads, num_sms, s, launches);
+  if (vpt == 2) return launch_norm<TX, TR, 2, false>(a, threads, num_sms, s, launches);
+  return launch_norm<TX, TR, 4, false>(a, threads, num_sms, s, launches);
+}
+
+template <int TX>
+cudaError_t launch_norm_residual(const NormArgs& a, int num_sms, cudaStream_t s, int* launches) {
+  switch (a.residual ? a.r_type : kTypeNone) {
+    case kTypeNone: return launch_norm_types<TX, kTypeNone>(a, num_sms, s, launches);
+    case kTypeF32: return launch_norm_types<TX, kTypeF32>(a, num_sms, s, launches);
+    case kTypeF16: return launch_norm_types<TX, kTypeF16>(a, num_sms, s, launches);
+    default: return launch_norm_types<TX, kTypeBf16>(a, num_sms, s, launches);
+  }
 }
 
 bool rows_aligned(const void* p, int64_t stride, int type) {
@@ -197,15 +228,9 @@ cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s, int*
   if (a.K % 8 == 0 && a.K <= 16384 && rows_aligned(a.X, a.x_stride, a.x_type) && rows_aligned(a.weight, 0, a.w_type) &&
       (a.out_type == kTypeE4m3 ? (reinterpret_cast<uintptr_t>(a.out) & 7u) == 0 : rows_aligned(a.out, a.K, a.out_type)) &&
       (!a.residual || (rows_aligned(a.residual, a.r_stride, a.r_type) && rows_aligned(a.residual_out, a.ro_stride, a.r_type)))) {
-    const int xb = type_bytes(a.x_type), rb = a.residual ? type_bytes(a.r_type) : 0;
-    if (xb == 2) {
-      if (rb == 0) return launch_norm_types<2, 0>(a, num_sms, s, launches);
-      if (rb == 2) return launch_norm_types<2, 2>(a, num_sms, s, launches);
-      return launch_norm_types<2, 4>(a, num_sms, s, launches);
-    }
-    if (rb == 0) return launch_norm_types<4, 0>(a, num_sms, s, launches);
-    if (rb == 2) return launch_norm_types<4, 2>(a, num_sms, s, launches);
-    return launch_norm_types<4, 4>(a, num_sms, s, launches);
+    if (a.x_type == kTypeF32) return launch_norm_residual<kTypeF32>(a, num_sms, s, launches);
+    if (a.x_type == kTypeF16) return launch_norm_residual<kTypeF16>(a, num_sms, s, launches);
+    return launch_norm_residual<kTypeBf16>(a, num_sms, s, launches);
   }
   const int threads = static_cast<int>(std::min<int64_t>(1024, ceil_div(a.K, 32) * 32));
   static unsigned long long done = 0;
