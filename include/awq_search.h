@@ -376,7 +376,7 @@ int awq_w4a16_dequant(const int32_t* codes, const void* steps, const void* zeros
  *   y[m][k] = h[m][k] weight[k] / sqrt(mean_k h[m][k]^2 + eps)   (statistics in fp32, of the
  *   unrounded h; rounded once to out_dtype)
  * X [M][K], residual and residual_out [M][K] (may be NULL together; residual_out may be
- * `residual` itself, otherwise it overlaps no other argument) and weight [K] each hold
+ * `residual` itself; otherwise it, and `out`, overlap no other argument) and weight [K] each hold
  * AWQ_DTYPE_F32, _F16 or _BF16; rows x_stride, r_stride and ro_stride apart. out [M][K]
  * contiguous holds one of these types, or AWQ_DTYPE_E4M3: out_scales[m] = max_k |y| / 448 (1
  * where that is zero) and out = e4m3(y / out_scales[m]); a row with a NaN or an infinity has
@@ -425,8 +425,8 @@ typedef struct awq_paged_cache {
 /* Token t of T, at positions[t] of sequence seqs[t] (seqs NULL: sequence t): writes
  * q_out[t] = rotated q[t] ([T][Hq][D] contiguous, AWQ_DTYPE_F16 or _BF16) and the rotated k[t]
  * and v[t] to the cache (e4m3: e4m3(x / scale), saturating at 448). q [T][Hq][D], k and v
- * [T][heads][D] hold in_dtype (F32, F16 or BF16), rows 16-byte aligned, e.g. the three parts of
- * one QKV product. Hq may be 0 (q, q_out unused). The pairs of dims (i, i + rotary_dim / 2),
+ * [T][heads][D] hold in_dtype (F32, F16 or BF16), rows 16-byte aligned and head strides below 2^29,
+ * e.g. the three parts of one QKV product. Hq may be 0 (q, q_out unused). The pairs of dims (i, i + rotary_dim / 2),
  * or (2 i, 2 i + 1) if `interleaved`, i < rotary_dim / 2, are turned by positions[t] * freqs[i]
  * (DEVICE doubles; the product is taken in fp64) and multiplied by `magnitude`; dims from
  * rotary_dim (a multiple of 16, at most D; 0 turns nothing) on are copied. A negative

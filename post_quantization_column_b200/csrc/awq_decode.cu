@@ -4,6 +4,7 @@
 #include "../../include/awq_search.h"
 #include "decode_kernels.h"
 
+#include <algorithm>
 #include <cmath>
 
 namespace {
@@ -55,15 +56,16 @@ int take_cache(const awq_paged_cache* in, PagedCache* out) {
   if (in->max_pages > (kIntMax - 1024) / in->page_size)
     return decode_error(AWQ_ERR_SHAPE, "a block table row names 2^31 tokens or more");
   const int64_t per32 = 32 / type_bytes(static_cast<int>(in->dtype));
-  if (!aligned(in->k, 32) || !aligned(in->v, 32) || in->page_stride % per32 || in->slot_stride % per32 ||
-      in->head_stride % per32)
+  // the stride of a dim of one is never taken
+  const int64_t strides[3] = {in->num_pages > 1 ? in->page_stride : 0, in->page_size > 1 ? in->slot_stride : 0,
+                              in->heads > 1 ? in->head_stride : 0};
+  if (!aligned(in->k, 32) || !aligned(in->v, 32) || strides[0] % per32 || strides[1] % per32 || strides[2] % per32)
     return decode_error(AWQ_ERR_INVALID_ARG, "the cache's rows must be 32-byte aligned");
-  if (in->page_stride < 0 || in->slot_stride < 0 || in->head_stride < 0 || in->table_stride < 0)
+  if (strides[0] < 0 || strides[1] < 0 || strides[2] < 0 || in->table_stride < 0)
     return decode_error(AWQ_ERR_INVALID_ARG, "strides must not be negative");
   // places within the cache are counted in units of 32 bytes, in 32 bits; a division keeps the
   // check itself from overflowing
   const int64_t room = ((int64_t(1) << 32) - 2) * per32 - in->head_dim, steps[3] = {in->num_pages - 1, in->page_size - 1, in->heads - 1};
-  const int64_t strides[3] = {in->page_stride, in->slot_stride, in->head_stride};
   int64_t span = 0;
   for (int i = 0; i < 3; ++i) {
     if (steps[i] > 0 && strides[i] > (room - span) / steps[i])
@@ -75,9 +77,9 @@ int take_cache(const awq_paged_cache* in, PagedCache* out) {
   out->k = in->k;
   out->v = in->v;
   out->num_pages = in->num_pages;
-  out->page_stride = in->page_stride;
-  out->slot_stride = in->slot_stride;
-  out->head_stride = in->head_stride;
+  out->page_stride = strides[0];
+  out->slot_stride = strides[1];
+  out->head_stride = strides[2];
   out->page_size = static_cast<int>(in->page_size);
   out->heads = static_cast<int>(in->heads);
   out->head_dim = static_cast<int>(in->head_dim);
@@ -119,10 +121,13 @@ int awq_rms_norm_on(int device, const void* X, int x_dtype, int64_t x_stride, co
   if (residual) {
     const bool same = residual == residual_out && r_stride == ro_stride;
     if ((!same && ranges_meet(residual, r_stride * rb, K * rb, residual_out, ro_stride * rb, K * rb, M)) ||
-        ranges_meet(X, x_stride * xb, K * xb, residual_out, ro_stride * rb, K * rb, M) ||
-        ranges_meet(out, K * ob, K * ob, residual_out, ro_stride * rb, K * rb, M))
+        ranges_meet(X, x_stride * xb, K * xb, residual_out, ro_stride * rb, K * rb, M))
       return decode_error(AWQ_ERR_INVALID_ARG, "residual_out may be the residual itself but overlap nothing else");
   }
+  if (ranges_meet(X, x_stride * xb, K * xb, out, K * ob, K * ob, M) ||
+      (residual && (ranges_meet(residual, r_stride * rb, K * rb, out, K * ob, K * ob, M) ||
+                    ranges_meet(residual_out, ro_stride * rb, K * rb, out, K * ob, K * ob, M))))
+    return decode_error(AWQ_ERR_INVALID_ARG, "out must not overlap another argument");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DeviceRestore restore_device;
   const void* ptrs[] = {X, residual, residual_out, weight, out, out_dtype == kTypeE4m3 ? out_scales : nullptr};
@@ -221,6 +226,8 @@ int awq_kv_append_on(int device, const void* q, int64_t q_token_stride, int64_t 
   if (q_token_stride < 0 || q_head_stride < 0 || k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 ||
       v_head_stride < 0)
     return decode_error(AWQ_ERR_INVALID_ARG, "strides must not be negative");
+  if (std::max(q_head_stride, std::max(k_head_stride, v_head_stride)) > kIntMax / 4)
+    return decode_error(AWQ_ERR_SHAPE, "the head strides of q, k and v must be below 2^29");
   const int64_t D = a.c.head_dim;
   if ((a.c.num_pages > 1 && a.c.page_stride < D) || (a.c.page_size > 1 && a.c.slot_stride < D) ||
       (a.c.heads > 1 && a.c.head_stride < D))
@@ -237,11 +244,12 @@ int awq_kv_append_on(int device, const void* q, int64_t q_token_stride, int64_t 
   a.k = k;
   a.v = v;
   a.q_st = q_token_stride;
-  a.q_sh = q_head_stride;
   a.k_st = k_token_stride;
-  a.k_sh = k_head_stride;
   a.v_st = v_token_stride;
-  a.v_sh = v_head_stride;
+  a.q_head = static_cast<uint32_t>(q_head_stride * type_bytes(in_dtype));
+  a.k_head = static_cast<uint32_t>(k_head_stride * type_bytes(in_dtype));
+  a.v_head = static_cast<uint32_t>(v_head_stride * type_bytes(in_dtype));
+  a.cache_head32 = static_cast<uint32_t>(a.c.head_stride * type_bytes(a.c.type) / 32);
   a.T = T;
   a.Hq = Hq;
   a.in_type = in_dtype;

@@ -55,7 +55,9 @@ struct AppendArgs {
   const void* q;  // [T][Hq][D], token and head strides in elements
   const void* k;
   const void* v;
-  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
+  int64_t q_st, k_st, v_st;
+  uint32_t q_head, k_head, v_head;  // the head strides in bytes
+  uint32_t cache_head32;            // the cache's in units of 32 bytes
   int64_t T;
   int Hq, in_type, q_type, rot, interleaved;
   const double* freqs;       // [rot / 2] radians per position

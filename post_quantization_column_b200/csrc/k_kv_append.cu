@@ -42,7 +42,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a)
   const int units = (a.Hq + 2 * c.heads) << shift;
   wait_for_previous();
   start_next();
-  const int64_t q_at = t * a.q_st, k_at = t * a.k_st, v_at = t * a.v_st;
+  constexpr int B = type_bytes(IN);
+  const uint8_t *q = static_cast<const uint8_t*>(a.q) + t * a.q_st * B, *k = static_cast<const uint8_t*>(a.k) + t * a.k_st * B,
+                *v = static_cast<const uint8_t*>(a.v) + t * a.v_st * B;
   Raw8<IN> r0[U], r1[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -51,10 +53,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a)
     const int head = w >> shift, u = w & ((1 << shift) - 1), kh = head - a.Hq, vh = kh - c.heads;
     int d0, d1;
     unit_dims(u, a.rot, vh < 0 && !a.interleaved, &d0, &d1);
-    const void* src = kh < 0 ? a.q : (vh < 0 ? a.k : a.v);
-    const int64_t at = kh < 0 ? q_at + head * a.q_sh : (vh < 0 ? k_at + kh * a.k_sh : v_at + vh * a.v_sh);
-    r0[i].load(src, at + d0);
-    r1[i].load(src, at + d1);
+    const uint8_t* src = kh < 0 ? q : (vh < 0 ? k : v);
+    const uint32_t step = kh < 0 ? a.q_head : (vh < 0 ? a.k_head : a.v_head), hh = kh < 0 ? head : (vh < 0 ? kh : vh);
+    src += static_cast<uint64_t>(hh) * step;
+    r0[i].load(src, d0);
+    r1[i].load(src, d1);
   }
   const int pos = a.positions[t];
   const int64_t seq = a.seq ? a.seq[t] : t;
@@ -68,16 +71,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a)
     sSin[threadIdx.x] = __fmul_rn(a.magnitude, sn);
   }
   // where the token's keys and values go
-  int64_t row = -1;
+  int64_t row = -1;  // bytes
   if (pos >= 0) {
     const int pi = pos / c.page_size;
     if (seq >= 0 && seq < c.seqs && pi < c.max_pages) {
       const int64_t page = c.table[seq * c.table_stride + pi];
       if (page >= 0 && page < c.num_pages)
-        row = page * c.page_stride + static_cast<int64_t>(pos - pi * c.page_size) * c.slot_stride;
+        row = (page * c.page_stride + static_cast<int64_t>(pos - pi * c.page_size) * c.slot_stride) * type_bytes(CACHE);
     }
     if (row < 0 && a.status && threadIdx.x == 0 && blockIdx.y == 0) *a.status = 1;
   }
+  uint16_t* q_out = static_cast<uint16_t*>(a.q_out) + t * a.Hq * D;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -115,17 +119,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a)
       }
     }
     if (kh < 0) {
-      const int64_t to = (t * a.Hq + head) * D;
       if (pos < 0) {  // a padded row of the batch
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = y[k] = 0.0f;
       }
+      uint16_t* to = q_out + head * D;
       if (a.q_type == kTypeBf16) {
-        store8_as<kTypeBf16>(a.q_out, to + d0, x);
-        store8_as<kTypeBf16>(a.q_out, to + d1, y);
+        store8_as<kTypeBf16>(to, d0, x);
+        store8_as<kTypeBf16>(to, d1, y);
       } else {
-        store8_as<kTypeF16>(a.q_out, to + d0, x);
-        store8_as<kTypeF16>(a.q_out, to + d1, y);
+        store8_as<kTypeF16>(to, d0, x);
+        store8_as<kTypeF16>(to, d1, y);
       }
     } else if (row >= 0) {
       const int hh = vh < 0 ? kh : vh;
@@ -137,10 +141,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a)
           y[k] = __fdiv_rn(y[k], scale);
         }
       }
-      void* dst = vh < 0 ? c.k : c.v;
-      const int64_t to = row + hh * c.head_stride;
-      store8_as<CACHE>(dst, to + d0, x);
-      store8_as<CACHE>(dst, to + d1, y);
+      uint8_t* dst = static_cast<uint8_t*>(vh < 0 ? c.k : c.v) + row + static_cast<uint64_t>(static_cast<uint32_t>(hh) * a.cache_head32) * 32u;
+      store8_as<CACHE>(dst, d0, x);
+      store8_as<CACHE>(dst, d1, y);
     }
   }
 }

@@ -29,19 +29,23 @@ __device__ __forceinline__ RowStat join(RowStat a, RowStat b) {
   return a;
 }
 
-// The statistic of a row whose parts the block's threads hold, in every thread.
-__device__ __forceinline__ RowStat block_join(RowStat a, RowStat* shared) {
+__device__ __forceinline__ RowStat warp_join(RowStat a) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     a = join(a, {__shfl_xor_sync(~0u, a.ss, o), __shfl_xor_sync(~0u, a.peak, o)});
-  const int warps = blockDim.x / 32;
-  if (warps == 1) return a;
-  if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = a;
-  __syncthreads();
-  a = shared[0];
-  for (int w = 1; w < warps; ++w) a = join(a, shared[w]);
-  __syncthreads();  // the slots are free for the next row
   return a;
+}
+
+// The statistic of a row whose parts the block's warps hold, in every thread. Rows take turns
+// between two sets of slots, so that one barrier a row is enough.
+__device__ __forceinline__ RowStat block_join(RowStat a, RowStat (*shared)[32], int& turn) {
+  const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
+  if (warps == 1) return a;
+  RowStat* slots = shared[turn];
+  turn ^= 1;
+  if (lane == 0) slots[threadIdx.x / 32] = a;
+  __syncthreads();
+  return warp_join(lane < warps ? slots[lane] : RowStat{0.0f, 0u});
 }
 
 __device__ __forceinline__ float row_factor(float ss, int64_t K, float eps) {
@@ -53,25 +57,71 @@ __device__ __forceinline__ float row_scale(uint32_t peak, float factor) {
   return scale == 0.0f ? 1.0f : scale;
 }
 
+// Vector v of the weight.
+__device__ __forceinline__ void load_weight(const NormArgs& a, int v, float (&w)[8]) {
+  if (a.w_type == kTypeF32) {
+    const float4* from = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + 8 * v);
+    const float4 lo = from[0], hi = from[1];
+    w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
+    w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + 8 * v);
+    const uint32_t words[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack16(words[k], a.w_type);
+      w[2 * k] = f.x;
+      w[2 * k + 1] = f.y;
+    }
+  }
+}
+
+// The thread's vectors h w of row m, with the row's statistic, to the output.
+template <int VPT>
+__device__ __forceinline__ void write_row(const NormArgs& a, int64_t m, int lane, int width, int vecs, RowStat st, float (&h)[VPT][8]) {
+  const float factor = row_factor(st.ss, a.K, a.eps);
+  if (a.out_type == kTypeE4m3) {
+    const float scale = row_scale(st.peak, factor);
+    if (lane == 0) a.out_scales[m] = scale;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = lane + i * width;
+      if (v >= vecs) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[i][k] = __fdiv_rn(__fmul_rn(h[i][k], factor), scale);
+      store8_as<kTypeE4m3>(a.out, m * a.K + 8 * v, h[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = lane + i * width;
+      if (v >= vecs) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[i][k] = __fmul_rn(h[i][k], factor);
+      store8(a.out, m * a.K + 8 * v, a.out_type, h[i]);
+    }
+  }
+}
+
 // Rows of aligned vectors of 8 values: the whole row lies in the registers of its threads, VPT
 // vectors each, between the reduction and the output. A row belongs to a warp (WARP, 8 rows a
 // block) or to a block; several blocks an SM load while others reduce, and the weight stays in
 // the L1 cache, which the rows themselves pass by.
 constexpr int norm_threads(bool warp) { return warp ? 256 : 512; }  // of a block, at most
-constexpr int norm_blocks(int vpt, bool warp) { return (warp ? 2 : 1) * (vpt == 1 ? 3 : (vpt == 2 ? 2 : 1)); }  // of that size an SM
+constexpr int norm_blocks(int vpt, bool warp) { return (warp ? 2 : 1) * (vpt <= 2 ? 2 : 1); }  // of that size an SM
 template <int TX, int TR, int VPT, bool WARP>
 __global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) norm_kernel(NormArgs a) {
-  __shared__ RowStat parts[16];
+  __shared__ RowStat parts[2][32];
+  int turn = 0;
   const int lane = WARP ? threadIdx.x % 32 : threadIdx.x, width = WARP ? 32 : blockDim.x;
   const int rows = WARP ? blockDim.x / 32 : 1;
   const int vecs = static_cast<int>(a.K / 8);
   const bool codes = a.out_type == kTypeE4m3;
   wait_for_previous();
   start_next();
-  for (int64_t m = static_cast<int64_t>(blockIdx.x) * rows + (WARP ? threadIdx.x / 32 : 0); m < a.M;
-       m += static_cast<int64_t>(gridDim.x) * rows) {
-    Raw8<TX> rx[VPT];
-    Raw8<TR == kTypeNone ? kTypeF16 : TR> rr[VPT];
+  Raw8<TX> rx[VPT];
+  Raw8<TR == kTypeNone ? kTypeF16 : TR> rr[VPT];
+  auto load_row = [&](int64_t m) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = lane + i * width;
@@ -80,6 +130,11 @@ __global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) no
         if (TR != kTypeNone) rr[i].load(a.residual, m * a.r_stride + 8 * v);
       }
     }
+  };
+  int64_t m = static_cast<int64_t>(blockIdx.x) * rows + (WARP ? threadIdx.x / 32 : 0);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+  if (m < a.M) load_row(m);
+  for (; m < a.M; m += step) {
     float h[VPT][8];
     RowStat st{0.0f, 0u};
 #pragma unroll
@@ -97,21 +152,7 @@ __global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) no
 #pragma unroll
       for (int k = 0; k < 8; ++k) st.ss = __fmaf_rn(h[i][k], h[i][k], st.ss);
       float w[8];
-      if (a.w_type == kTypeF32) {
-        const float4* from = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + 8 * v);
-        const float4 lo = from[0], hi = from[1];
-        w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
-        w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
-      } else {
-        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + 8 * v);
-        const uint32_t words[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = unpack16(words[k], a.w_type);
-          w[2 * k] = f.x;
-          w[2 * k + 1] = f.y;
-        }
-      }
+      load_weight(a, v, w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) h[i][k] = __fmul_rn(h[i][k], w[k]);
       if (codes) {
@@ -119,35 +160,10 @@ __global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) no
         for (int k = 0; k < 8; ++k) st.peak = max(st.peak, __float_as_uint(h[i][k]) & 0x7FFFFFFFu);
       }
     }
-    if (WARP) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        st = join(st, {__shfl_xor_sync(~0u, st.ss, o), __shfl_xor_sync(~0u, st.peak, o)});
-    } else {
-      st = block_join(st, parts);
-    }
-    const float factor = row_factor(st.ss, a.K, a.eps);
-    if (codes) {
-      const float scale = row_scale(st.peak, factor);
-      if (lane == 0) a.out_scales[m] = scale;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = lane + i * width;
-        if (v >= vecs) continue;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) h[i][k] = __fdiv_rn(__fmul_rn(h[i][k], factor), scale);
-        store8_as<kTypeE4m3>(a.out, m * a.K + 8 * v, h[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = lane + i * width;
-        if (v >= vecs) continue;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) h[i][k] = __fmul_rn(h[i][k], factor);
-        store8(a.out, m * a.K + 8 * v, a.out_type, h[i]);
-      }
-    }
+    if (m + step < a.M) load_row(m + step);  // on the way during the reduction and the output
+    st = warp_join(st);
+    if (!WARP) st = block_join(st, parts, turn);
+    write_row<VPT>(a, m, lane, width, vecs, st, h);
   }
 }
 
@@ -155,7 +171,8 @@ __global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) no
 // h stays in shared memory between the two uses of it.
 __global__ void __launch_bounds__(1024) norm_any_kernel(NormArgs a) {
   extern __shared__ float h_row[];
-  __shared__ RowStat parts[32];
+  __shared__ RowStat parts[2][32];
+  int turn = 0;
   wait_for_previous();
   start_next();
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
@@ -170,7 +187,7 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(NormArgs a) {
       h_row[k] = hw;
       st = join(st, {__fmul_rn(h, h), __float_as_uint(hw) & 0x7FFFFFFFu});
     }
-    st = block_join(st, parts);
+    st = block_join(warp_join(st), parts, turn);
     const float factor = row_factor(st.ss, a.K, a.eps);
     const float scale = a.out_type == kTypeE4m3 ? row_scale(st.peak, factor) : 1.0f;
     if (a.out_type == kTypeE4m3 && threadIdx.x == 0) a.out_scales[m] = scale;

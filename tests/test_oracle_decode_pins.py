@@ -97,7 +97,8 @@ def test_rms_norm_refusals():
                    (dict(M=1 << 31), 2), (dict(xt=3), 1), (dict(wt=4), 1), (dict(ot=4), 1), (dict(ot=3), 1), (dict(eps=-1.0), 1),
                    (dict(eps=math.nan), 1), (dict(eps=math.inf), 1), (dict(r=P), 1), (dict(ro=P), 1), (dict(X=P + 2), 1),
                    (dict(out=P + 1), 1), (dict(xs=-1), 1), (dict(r=P + 512, ro=P + 512, ros=100), 1),
-                   (dict(r=P, ro=P + 64), 1), (dict(r=P + 1024, ro=P), 1), (dict(r=P + 1024, rt=7, ro=P + 1024), 1)):
+                   (dict(r=P, ro=P + 64), 1), (dict(r=P + 1024, ro=P), 1), (dict(r=P + 1024, rt=7, ro=P + 1024), 1),
+                   (dict(out=P + 1000), 1), (dict(r=P + 1024, ro=P + 1024, out=P + 1536), 1)):
         assert _norm(**kw) == st, kw
         assert lib.awq_last_error_message()
     assert _norm(M=0, X=NULL, out=NULL) == 0
@@ -128,7 +129,7 @@ def test_kv_append_refusals():
     for kw, st in ((dict(k=NULL), 1), (dict(v=NULL), 1), (dict(pos=NULL), 1), (dict(q=NULL), 1), (dict(qo=NULL), 1), (dict(it=3), 1),
                    (dict(qt=1), 1), (dict(T=-1), 2), (dict(Hq=-1), 2), (dict(rot=24), 2), (dict(rot=144), 2), (dict(rot=-16), 2),
                    (dict(f=NULL), 1), (dict(mag=math.inf), 1), (dict(T=4), 2), (dict(qs=4), 1), (dict(k=P + 8), 1),
-                   (dict(vh=-128), 1), (dict(pos=P + 2), 1), (dict(f=P + 4), 1), (dict(st=P + 1), 1), (dict(c=NULL), 1)):
+                   (dict(vh=-128), 1), (dict(kh=1 << 29), 2), (dict(pos=P + 2), 1), (dict(f=P + 4), 1), (dict(st=P + 1), 1), (dict(c=NULL), 1)):
         assert _append(**kw) == st, kw
     for kw in (dict(ps=0), dict(ss=64), dict(hs=0)):   # a written cache with rows on one another
         assert _append(_cache(**kw)) == 1
