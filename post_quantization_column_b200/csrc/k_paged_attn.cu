@@ -6,27 +6,39 @@
 // met so far (the sums are rescaled when it grows), so the cache is read once. Every group
 // of Hq / Hkv query heads shares its key-value head's bytes: they are read once for the group.
 //
-// What bounds it: the cache's bytes (2 D bytes of keys and as much of values per token and
-// key-value head, against 4 D multiply-adds per query head), so the kernel is a stream.
+// What bounds it: the cache's bytes (each of 2 D values per token and key-value head is used in
+// Hq / Hkv multiply-adds), so the kernel is a stream.
 //
-// Work. The unit is 64 tokens of one (sequence, key-value head): all units of the batch,
-// sequence-major, are dealt to a grid of as many CTAs as fit the SMs, in equal contiguous
-// runs, whatever the lengths are. A CTA finds its run from the lengths on the device. A
-// (sequence, head) that lies within one run is finished there; one that crosses runs leaves
-// a partial (o, m, l) per run, and a second kernel adds them in run order (fixed order:
-// equal inputs give equal bits).
+// Work. The unit is 32 KB of the cache: 64 tokens of one (sequence, key-value head) at D = 128
+// in 16 bits, more where rows are shorter. All units of the batch, sequence-major, are dealt to
+// a grid of as many CTAs as fit the SMs, in equal contiguous runs, whatever the lengths are; a CTA
+// finds its run from the lengths on the device. A (sequence, head) that lies within one run is
+// finished there; one that crosses runs leaves a partial (o, m, l) per run, and a second
+// kernel adds them in run order (fixed order: equal inputs give equal bits). That join costs
+// 3 to 5 us, so where the longest sequence has at most kWhole units runs begin and end with
+// segments instead (55 sequences of 128 tokens, 8 heads: 8.7 us against 12.4 cut and joined).
 //
-// Tile. A warp takes 16 tokens (more where rows are short: 8 KB of cache) of a unit with its
-// own running maximum; the four warps meet once per (sequence, head). Tokens are the rows of
-// both products, so a group of up to 8 heads fills the 8 columns of an m16n8k16 MMA and none
-// of the 16 rows is padding:
+// Tile. A warp takes 8 KB (16 tokens at D = 128 in 16 bits) of a unit with its own running
+// maximum; the four warps meet once per (sequence, head). Tokens are the rows of both products,
+// so a group of up to 8 heads fills the 8 columns of an m16n8k16 MMA and none of the 16 rows is
+// padding:
 //   S^T (16 tokens x 8 heads) = K Q^T,   O^T (16 dims x 8 heads) += V^T P^T.
 // The sum over dims in q . k may run in any order and the rows of O^T may be any dims, so
-// each lane is given dims that lie together in memory: 16-byte pieces of the cache rows are
+// each lane is given dims that lie together in memory: 32-byte pieces of the cache rows are
 // its MMA fragments as they are (keys) or after a byte shuffle of two tokens' words (values).
 // The cache therefore goes from memory to the fragments' registers without shared memory: a
 // warp loads the keys of its next tile when it has used these keys, the next values when it
-// has used these values, and the twelve warps of an SM keep some 90 KB on the way.
+// has used these values, and the twelve warps of an SM keep some 90 KB on the way. (A ring of
+// cp.async stages took twice the time: eight warps' chains of shared-memory reads, shuffles
+// and products were longer than the loads; bulk copies of 128-byte rows stop at 3.9 TB/s.)
+// The MMAs are mma.sync: tcgen05 wants 64 rows or more of a tile in shared memory, and at one
+// token per sequence the tensor pipe is 4 % busy here.
+//
+// Measured (B200, device time in a captured graph; the copy rate is 6.55 TB/s): 16 x 4096 tokens
+// of 32 fp16 heads 162 us, 6.6 TB/s; 67 ragged sequences up to 8192, 8 bf16 heads shared by 64,
+// 189 us, 6.4 TB/s; one sequence of 131072 tokens 88 us, 6.1 TB/s; 96 ragged sequences up to
+// 4099 on an e4m3 cache 95 us, 4.6 TB/s (bound by the latency of a tile's chain: 131 of its 560
+// instructions unpack e4m3; 6.7 TB/s at the margin of longer sequences); one of 33 tokens 4.8 us.
 #include "decode_kernels.h"
 
 #include <algorithm>
@@ -39,6 +51,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 3 * 148;  // three CTAs on each of a B200's SMs
 constexpr int kWhole = 4;           // units of the longest segment that is not cut
+constexpr int kLong = 40;           // units a CTA from which heads lie side by side
 
 template <int D, int TYPE, int NB>
 struct Tile {
@@ -51,6 +64,7 @@ struct Tile {
   static constexpr int kBlocks = 256 / (D * ES) > 1 ? 256 / (D * ES) : 1;  // blocks of 16 tokens of a warp's tile
   static constexpr int kTok = 16 * kBlocks;
   static constexpr bool kShort = D * ES <= 128;                      // rows of which a CTA may take several heads'
+  static constexpr int kSub = kShort ? kWarps : 1;                   // places of a run's partial sums
   static constexpr int kHeads = NB * 8;                              // query heads of a work segment
   static constexpr int kPitch = D + 2;                               // floats between heads in the join buffer
   static constexpr int kCtas = D * NB > 128 || (D == 64 && NB == 2) ? 2 : 3;                // per SM, by registers
@@ -142,18 +156,18 @@ struct Cursor {
 };
 
 struct Space {       // the work space of a launch
-  float* o;          // [2 C][heads][D] partial sums of run c: slot 2 c of the segment that begins in it and
+  float* o;          // [2 C][kSub][heads][D] partial sums of run c: slot 2 c of the segment that begins in it and
                      // goes on, slot 2 c + 1 of the one that began before it
-  float2* ml;        // [2 C][heads] (m, l)
-  int4* joins;       // what the second kernel joins: pieces (0: nothing), first run, sequence, head block;
-                     // one per segment if there are no more segments than CTAs, else one per CTA
+  float2* ml;        // [2 C][kSub][heads] (m, l)
+  int4* joins;       // what the second kernel joins: pieces (0: nothing), the first piece's place, sequence, head
+                     // block; one per segment if there are no more segments than CTAs, else kSub per CTA
 };
 
 struct Geometry {
   int cap;           // tokens a table row can name
   int heads_per;     // Hq / Hkv
   int hgroups;       // blocks of query heads per key-value head
-  int side;          // key-value heads side by side in a CTA: 1, 2 or 4, of kWarps / side warps each
+  int side;          // key-value heads that may lie side by side in a CTA: 1, 2 or 4, of kWarps / side warps each
   int64_t ctas;
   int by_segment;    // the joins are listed by segment
   int64_t listed;
@@ -167,7 +181,7 @@ template <int D, int TYPE, int NB, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
     paged_attn_kernel(PagedAttnArgs a, Geometry geo, Space sp) {
   using T_ = Tile<D, TYPE, NB>;
-  constexpr int ES = T_::ES, KB = T_::kKBytes, KC = T_::kKChunks, VB = T_::kVBytes, VC = T_::kVChunks, S = T_::kSteps, TB = T_::kBlocks;
+  constexpr int ES = T_::ES, KB = T_::kKBytes, KC = T_::kKChunks, VB = T_::kVBytes, VC = T_::kVChunks, S = T_::kSteps, TB = T_::kBlocks, SUB = T_::kSub;
   constexpr int kTok = T_::kTok;
   constexpr int MMA = TYPE == kTypeBf16 ? kTypeBf16 : kTypeF16;
   // The maximum in use may lag behind the scores by 2^kLag before the sums are rescaled: weights
@@ -183,41 +197,52 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t = lane & 3;
   const PagedCache& c = a.c;
-  const int side = T_::kShort ? geo.side : 1, unit = kTok * kWarps / side;
-  const int HH = c.heads / side * geo.hgroups;
-  const int deep = kWarps / side, head_of = warp / deep, tok_of = warp % deep * kTok;  // the warp's head and tokens of a unit
-
   wait_for_previous();
   start_next();  // the join is set up meanwhile
 
   // ---- the run: exclusive sums of the sequences' units, then the places of its two ends
   const int64_t per = ceil_div(a.B, kThreads), b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-  int64_t mine = 0;
-  int longest = 0;
-  for (int64_t b = b0; b < b1; ++b) {
-    const int nblk = (clamped_length(a.lengths, b, geo.cap) + unit - 1) / unit;
-    mine += nblk;
-    longest = max(longest, nblk);
-  }
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += up;
-  }
-  longest = __reduce_max_sync(~0u, longest);
-  if (lane == 31) {
-    sScan[warp] = incl;
-    sBad[warp] = longest;
-  }
   if (tid < 2) sSnap[tid] = 0;
-  __syncthreads();
-  int64_t before = incl - mine, total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sScan[w];
-    total += sScan[w];
-    longest = max(longest, sBad[w]);
+  int64_t mine, before, total;
+  int longest;
+  auto count_units = [&](int unit) {
+    mine = 0;
+    longest = 0;
+    for (int64_t b = b0; b < b1; ++b) {
+      const int nblk = (clamped_length(a.lengths, b, geo.cap) + unit - 1) / unit;
+      mine += nblk;
+      longest = max(longest, nblk);
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += up;
+    }
+    longest = __reduce_max_sync(~0u, longest);
+    if (lane == 31) {
+      sScan[warp] = incl;
+      sBad[warp] = longest;
+    }
+    __syncthreads();
+    before = incl - mine;
+    total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sScan[w];
+      total += sScan[w];
+      longest = max(longest, sBad[w]);
+    }
+  };
+  int side = 1;
+  count_units(kTok * kWarps);
+  if (T_::kShort && geo.side > 1 && total * c.heads * geo.hgroups >= kLong * geo.ctas) {
+    side = geo.side;
+    __syncthreads();  // the sums have been read
+    count_units(kTok * kWarps / side);
   }
+  const int unit = kTok * kWarps / side;
+  const int HH = c.heads / side * geo.hgroups;
+  const int deep = kWarps / side, head_of = warp / deep, tok_of = warp % deep * kTok;  // the warp's head and tokens of a unit
   // No run is empty: with fewer units than CTAs the later CTAs have none. Where segments are short a
   // run begins and ends with one instead (and may be empty): a join takes longer than kWhole units.
   const int64_t units = total * HH, C = min(geo.ctas, units);
@@ -249,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x)
     if (a.lengths[b] <= 0) {
       if (geo.by_segment)
-        for (int i = tid; i < HH; i += kThreads) sp.joins[b * HH + i] = make_int4(0, 0, 0, 0);
+        for (int i = tid; i < c.heads * geo.hgroups; i += kThreads) sp.joins[b * c.heads * geo.hgroups + i] = make_int4(0, 0, 0, 0);
       for (int64_t i = tid; i < static_cast<int64_t>(a.Hq) * D / 2; i += kThreads)
         static_cast<uint32_t*>(a.out)[b * a.Hq * D / 2 + i] = 0u;
     }
@@ -257,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   const int64_t u0 = ends_at[0] + sSnap[0];
   const int n = static_cast<int>(ends_at[1] + sSnap[1] - u0);
   if (n <= 0) {
-    if (tid == 0 && !geo.by_segment) sp.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (tid < SUB && !geo.by_segment) sp.joins[blockIdx.x * SUB + tid] = make_int4(0, 0, 0, 0);
     return;
   }
 
@@ -614,16 +639,15 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
       const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (seg0 < u0 ? 1 : 0);
       const int hb = cc.hg * T_::kHeads;
       const int live = min(T_::kHeads, geo.heads_per - hb);
-      if (tid == 0) {
-        if (any_bad && a.status) *a.status = 1;
-        const bool begins = seg0 >= u0;
-        if (geo.by_segment ? begins : last) {
-          const int hh = cc.kg * geo.hgroups + cc.hg;
-          int pieces = 0;
-          if (begins && !ends)
-            pieces = static_cast<int>(unit_owner(seg0 + (cc.len + unit - 1) / unit - 1, units, C) - blockIdx.x) + 1;
-          sp.joins[geo.by_segment ? static_cast<int64_t>(cc.b) * HH + hh : blockIdx.x] = make_int4(pieces, blockIdx.x, cc.b, hh);
-        }
+      if (any_bad && tid == 0 && a.status) *a.status = 1;
+      const bool begins = seg0 >= u0;
+      if (tid < SUB && (geo.by_segment ? begins && tid < side : last)) {
+        const int hh = (cc.kg * side + tid) * geo.hgroups + cc.hg;
+        int pieces = 0;
+        if (begins && !ends && tid < side)
+          pieces = static_cast<int>(unit_owner(seg0 + (cc.len + unit - 1) / unit - 1, units, C) - blockIdx.x) + 1;
+        const int64_t at = geo.by_segment ? static_cast<int64_t>(cc.b) * c.heads * geo.hgroups + hh : blockIdx.x * SUB + tid;
+        sp.joins[at] = make_int4(pieces, 2 * SUB * blockIdx.x + tid, cc.b, hh);
       }
       auto top_of = [&](int hs, int h) {  // the maximum of head h of the hs-th key-value head
         float top = sM[hs * deep][h];
@@ -670,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) =
                 make_uint2(pack16(o[0] * r, o[1] * r, a.q_type), pack16(o[2] * r, o[3] * r, a.q_type));
           } else {
-            const int64_t to = (part * side + hs) * T_::kHeads + h;
+            const int64_t to = (part * SUB + hs) * T_::kHeads + h;
             *reinterpret_cast<float4*>(sp.o + to * D + d) = make_float4(o[0], o[1], o[2], o[3]);
             if (d == 0) sp.ml[to] = make_float2(top, L);
           }
@@ -686,22 +710,20 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
 // The segments that cross runs: o = (sum over the runs, in order, of o_c 2^(m_c - m)) / l. D / 4
 // threads take a head's dims, four each, and `teams` teams of as many share its pieces out.
 constexpr int kJoinThreads = 256;
-template <int D, int HEADS>
+template <int D, int HEADS, int SUB>
 __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(PagedAttnArgs a, Geometry geo, Space sp, int teams) {
   constexpr int kTeam = D / 4, kAhead = 8;
   __shared__ float4 sO[kJoinThreads];
   __shared__ float2 sML[kJoinThreads / kTeam];
   const int tid = threadIdx.x, team = tid / kTeam, d = tid % kTeam * 4;
   const int per = kJoinThreads / kTeam / teams;          // heads of a CTA
-  const int rows = geo.side * HEADS;                     // heads of a listed segment
-  const int64_t head = static_cast<int64_t>(blockIdx.x) * per + team / teams;
-  const int64_t listed = head / rows;
-  const int r = static_cast<int>(head % rows);
+  const int64_t head = static_cast<int64_t>(blockIdx.x) * per + team / teams, listed = head / HEADS;
+  const int r = static_cast<int>(head % HEADS);
   wait_for_previous();
   start_next();
   const int4 job = listed < geo.listed ? sp.joins[listed] : make_int4(0, 0, 0, 0);
-  const int pieces = job.x, c0 = job.y;                  // no pieces: finished by its run
-  const int kvh = job.w / geo.hgroups * geo.side + r / HEADS, h = (job.w % geo.hgroups) * HEADS + r % HEADS;
+  const int pieces = job.x;                              // none: finished by its run
+  const int kvh = job.w / geo.hgroups, h = (job.w % geo.hgroups) * HEADS + r;
   const bool live = pieces > 0 && h < geo.heads_per;
   float top = kNoMax, L = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -721,7 +743,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(PagedAttn
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int p = min(p0 + k * teams, pieces - 1);
-        const int64_t at = (2 * static_cast<int64_t>(c0 + p) + (p > 0 ? 1 : 0)) * rows + r;  // it begins in run c0 and goes on
+        const int64_t at = (job.y + (2 * p + (p > 0 ? 1 : 0)) * SUB) * static_cast<int64_t>(HEADS) + r;  // it goes on in the next runs
         ml[k] = sp.ml[at];
         v[k] = *reinterpret_cast<const float4*>(sp.o + at * D + d);
       }
@@ -743,14 +765,19 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(PagedAttn
       make_uint2(pack16(o.x * x, o.y * x, a.q_type), pack16(o.z * x, o.w * x, a.q_type));
 }
 
-// Heads of a CTA: where the heads of a token lie side by side and a row is short, the four
-// warps take four heads of the same tokens instead of four runs of tokens of one head, so that
-// what is read at one time lies together.
-int heads_side_by_side(const PagedCache& c, int64_t segments) {
-  if (c.head_dim * type_bytes(c.type) > 128 || c.head_stride >= c.slot_stride || segments < kMaxCtas / 2) return 1;
+// Where the heads of a token lie side by side and rows are short, the four warps of a CTA can take
+// four heads of the same tokens instead of four runs of tokens of one head, so that what is read
+// at one time lies together in memory. It pays from some 40 units a CTA on (kLong; e4m3, D = 128,
+// 8 heads: 55 x 8192 tokens 161 against 165 us, 55 x 4096 91 against 88; 32 heads, 32 ragged
+// sequences up to 8192: 195 against 210 us), since the units are a quarter as deep and leave four
+// heads' partial sums where they cross runs.
+int heads_side_by_side(const PagedCache& c) {
+  if (c.head_dim * type_bytes(c.type) > 128 || c.head_stride >= c.slot_stride) return 1;
   return c.heads % 4 == 0 ? 4 : (c.heads % 2 == 0 ? 2 : 1);
 }
 
+// Blocks of 8 query heads that share a pass over the cache: two where a group has more than 8 and
+// the registers hold both. Larger groups read the cache again, from L2 for the most part.
 int head_blocks(int Hq, int Hkv, int D) { return Hq / Hkv > 8 && D <= 128 ? 2 : 1; }
 
 template <int D, int TYPE, int NB>
@@ -760,16 +787,16 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* lau
   geo.cap = static_cast<int>(std::min<int64_t>(a.c.max_pages * a.c.page_size, INT32_MAX - 1024));
   geo.heads_per = a.Hq / a.c.heads;
   geo.hgroups = static_cast<int>(ceil_div(geo.heads_per, T_::kHeads));
-  geo.side = heads_side_by_side(a.c, a.B * a.c.heads * geo.hgroups);
-  const int unit = T_::kTok * kWarps / geo.side;  // tokens of a unit
-  const int64_t segments = a.B * (a.c.heads / geo.side) * geo.hgroups;
+  geo.side = heads_side_by_side(a.c);
+  const int unit = T_::kTok * kWarps;  // tokens of a unit of one head
+  const int64_t segments = a.B * a.c.heads * geo.hgroups;
   geo.ctas = std::min<int64_t>(std::min(kMaxCtas, T_::kCtas * num_sms), segments * ceil_div(geo.cap, unit));
   geo.by_segment = segments <= geo.ctas;
-  geo.listed = std::min(segments, geo.ctas);
+  geo.listed = geo.by_segment ? segments : geo.ctas * T_::kSub;
   Space sp;
   sp.o = static_cast<float*>(a.workspace);
-  sp.ml = reinterpret_cast<float2*>(sp.o + 2 * kMaxCtas * geo.side * T_::kHeads * D);
-  sp.joins = reinterpret_cast<int4*>(sp.ml + 2 * kMaxCtas * geo.side * T_::kHeads);
+  sp.ml = reinterpret_cast<float2*>(sp.o + 2 * kMaxCtas * T_::kSub * T_::kHeads * D);
+  sp.joins = reinterpret_cast<int4*>(sp.ml + 2 * kMaxCtas * T_::kSub * T_::kHeads);
   const int es = type_bytes(TYPE);
   geo.page32 = static_cast<uint32_t>(a.c.page_stride * es / 32);
   geo.slot32 = static_cast<uint32_t>(a.c.slot_stride * es / 32);
@@ -784,10 +811,10 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* lau
   if (e != cudaSuccess) return e;
   if (geo.cap <= kWhole * unit) return cudaSuccess;  // no segment crosses runs
   // few segments have many pieces each: eight teams share a head's pieces out
-  const int64_t heads = geo.listed * geo.side * T_::kHeads;
+  const int64_t heads = geo.listed * T_::kHeads;
   const int teams = heads <= kMaxCtas ? std::min(8, kJoinThreads / (D / 4)) : 1;
   const dim3 grid(static_cast<unsigned>(ceil_div(heads * teams, kJoinThreads / (D / 4))));
-  return launch_early(paged_attn_join_kernel<D, T_::kHeads>, grid, kJoinThreads, 0, s, launches, a, geo, sp, teams);
+  return launch_early(paged_attn_join_kernel<D, T_::kHeads, T_::kSub>, grid, kJoinThreads, 0, s, launches, a, geo, sp, teams);
 }
 
 template <int D>
@@ -809,8 +836,8 @@ cudaError_t launch_d(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* l
 }  // namespace
 
 int64_t paged_attn_workspace(int Hq, int Hkv, int D, int type) {
-  const int64_t heads = head_blocks(Hq, Hkv, D) * 8 * (D * type_bytes(type) <= 128 ? 4 : 1);
-  return 2 * kMaxCtas * heads * (D * 4 + 8) + kMaxCtas * 16;
+  const int64_t places = kMaxCtas * (D * type_bytes(type) <= 128 ? kWarps : 1), heads = head_blocks(Hq, Hkv, D) * 8;
+  return places * (2 * heads * (D * 4 + 8) + 16);  // Space: partial sums, their (m, l), joins
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* launches) {

@@ -369,6 +369,37 @@ def test_attention_batches(lens):
     assert torch.equal(out, awq.paged_attention(q, kc, vc, table, lt))   # the same bits again
 
 
+@pytest.mark.parametrize("lens,Hq,H,Dh,page,qt,cache", [
+    ([35000] * 4 + [0] + [36001] * 4, 16, 8, 128, 32, F16, E4M3),        # few segments, heads in fours
+    ([4400 + 37 * (i % 9) for i in range(65)], 8, 8, 128, 16, BF16, E4M3),  # more segments than runs
+    ([130000, 0, 100001, 150000], 6, 6, 64, 64, F16, F16),               # rows of 128 bytes, heads in twos
+    ([90000, 60000, 80000], 20, 20, 64, 24, BF16, E4M3),                 # a page that ends inside a block of 16
+    ([200000, 230001], 5, 5, 64, 16, F16, E4M3)])                        # heads that do not pair
+def test_attention_long_batches_of_short_rows(lens, Hq, H, Dh, page, qt, cache):
+    """Enough work that the heads of short rows lie side by side in a CTA where they can."""
+    g = torch.Generator("cuda").manual_seed(Hq + Dh)
+    rng = np.random.default_rng(Dh)
+    B, need = len(lens), [-(-n // page) for n in lens]
+    pages = sum(need) + 1
+    scales = [torch.rand(H, device="cuda", generator=g) * 0.01 + 0.015 for _ in range(2)] if cache == E4M3 else [None, None]
+    caches = [(torch.randn(pages, page, H, Dh, device="cuda", generator=g, dtype=F16) * (50 if cache == E4M3 else 1)).to(cache) for _ in range(2)]
+    order, table, at = rng.permutation(pages).astype(np.int32), np.zeros((B, max(need)), dtype=np.int32), 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    q = _randn(B, Hq, Dh, dtype=qt, seed=3, scale=2.0)
+    lt, tab = torch.tensor(lens, dtype=torch.int32, device="cuda"), torch.from_numpy(table).cuda()
+    out = awq.paged_attention(q, *caches, tab, lt, k_scale=scales[0], v_scale=scales[1])
+    _check_attention(q, *caches, tab, lt, out, None, *scales, rows=sorted({0, B // 2, B - 1}))
+    assert torch.isfinite(out.float()).all()
+    # every row again, alone: another split of the same sums. Both are within E sum p |v - o| of the
+    # exact value, E < 1e-3 (an fp16 weight's half step and the score's error) and |v| about 1, and
+    # rounded to at most a half step of bf16
+    for b in range(B):
+        alone = awq.paged_attention(q[b:b + 1], *caches, tab[b:b + 1], lt[b:b + 1], k_scale=scales[0], v_scale=scales[1])
+        assert torch.allclose(alone[0].float(), out[b].float(), atol=2e-3, rtol=2e-2), b
+
+
 def test_attention_peaked_and_flat_scores():
     q, kc, vc, table, lens, _ = _attn_case([900, 130, 40], 4, 4, 128, 16, F16, F16, seed=5, spread=20.0)
     out = awq.paged_attention(q, kc, vc, table, lens)
@@ -451,6 +482,30 @@ def test_attention_bad_pages_and_lengths():
         with pytest.raises(awq.AwqError):
             awq.check_status(status)
     assert torch.isnan(awq.paged_attention(q, kc, vc, table, lt)[1].float()).all()   # and without a status word
+
+
+@pytest.mark.parametrize("lens,Hq,H,Dh,cache", [([5000] * 4, 8, 8, 128, F16), ([700] * 70, 8, 8, 128, E4M3), ([9000] * 66, 8, 8, 128, E4M3),
+                                                ([40000], 32, 2, 64, F16), ([900] * 100, 20, 5, 256, F16), ([65], 16, 1, 128, BF16)])
+def test_attention_stays_in_its_work_space(lens, Hq, H, Dh, cache):
+    """Through the C ABI, in exactly the bytes it asks for: what lies behind them stays."""
+    import ctypes
+    import struct
+    qt = F16 if cache == E4M3 else cache
+    q, kc, vc, table, lt, (ks, vs) = _attn_case(lens, Hq, H, Dh, 16, qt, cache, seed=Dh)
+    lib, code = awq.library(), {BF16: 0, F16: 2, E4M3: 3}
+    size = lib.awq_paged_attention_workspace(Hq, H, Dh, code[cache])
+    ws = torch.full((size + 65536,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = torch.full((len(lens) * Hq * Dh + 512,), 7.0, dtype=qt, device="cuda")
+    desc = struct.pack("@16q", kc.data_ptr(), vc.data_ptr(), code[cache], *kc.shape, *kc.stride()[:3], ks.data_ptr() if ks is not None else 0,
+                       vs.data_ptr() if vs is not None else 0, table.data_ptr(), *table.shape, table.stride(0))
+    torch.cuda.synchronize()
+    st = lib.awq_paged_attention(q.data_ptr(), q.stride(0), q.stride(1), code[qt], Hq, desc, lt.data_ptr(), Dh ** -0.5, out.data_ptr(),
+                                 ws.data_ptr(), size, None, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == 0, lib.awq_last_error_message()
+    torch.cuda.synchronize()
+    assert (ws[size:] == 0x5A).all() and (out[len(lens) * Hq * Dh:] == 7.0).all()
+    want = awq.paged_attention(q, kc, vc, table, lt, k_scale=ks, v_scale=vs)
+    assert torch.equal(out[: len(lens) * Hq * Dh].view_as(want), want)
 
 
 def test_attention_shared_pages_and_expanded_queries():
