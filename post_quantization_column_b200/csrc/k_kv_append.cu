@@ -9,6 +9,13 @@
 // fraction of a turn there, so that a position of a million loses no more than 1e-9 turns;
 // the sine and cosine of the fraction are fp32. Results are rounded once to the query's and
 // the cache's types (an e4m3 cache holds e4m3(x / scale) of its head's scale).
+//
+// What bounds it: the bytes of q, k and v, read and written once. The angles are worked out once
+// per block of a token, while its values are on the way; a thread turns 16 values of a head. In
+// a captured graph 4096 tokens of 32 + 2 x 32 bf16 heads take 36 us, 5.7 TB/s (address and
+// conversion instructions keep the issue slots half busy), 2047 tokens of 64 + 2 x 8 fp32 heads
+// 20 us, 6.3 TB/s, one token 2.4 us. A persistent form that loads the next token's values early
+// took 50 us for the former: its registers halve the blocks an SM holds.
 #include "decode_kernels.h"
 
 #include <algorithm>
@@ -16,7 +23,7 @@
 namespace awq {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 constexpr int kMaxRot = 256;
 
 // A unit is 16 values of one head: dims 8u .. 8u + 7 and rot/2 + 8u .. of a rotated half
@@ -34,7 +41,7 @@ __device__ __forceinline__ void unit_dims(int u, int rot, bool half_pairs, int* 
 // One token per blockIdx.x; each of the gridDim.y blocks of the token takes U units per thread
 // of its Hq + 2 Hkv heads, and has them on the way before it works out the angles.
 template <int IN, int CACHE, int U>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(AppendArgs a) {
   __shared__ __align__(16) float sCos[kMaxRot / 2], sSin[kMaxRot / 2];
   const int64_t t = blockIdx.x;
   const PagedCache& c = a.c;
@@ -62,7 +69,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a)
   const int pos = a.positions[t];
   const int64_t seq = a.seq ? a.seq[t] : t;
   const int half = a.rot / 2;
-  if (threadIdx.x < half) {  // rot <= 256: one angle per thread
+  static_assert(kMaxRot / 2 <= kAppendThreads, "one angle per thread");
+  if (threadIdx.x < half) {
     const double turns = static_cast<double>(pos) * a.freqs[threadIdx.x] * 0.15915494309189533577;  // 1 / (2 pi)
     const float frac = static_cast<float>(turns - rint(turns));
     float sn, cs;
@@ -152,11 +160,12 @@ template <int IN, int CACHE>
 cudaError_t launch(const AppendArgs& a, int num_sms, cudaStream_t s, int* launches) {
   const int units = (a.Hq + 2 * a.c.heads) * (a.c.head_dim / 16);
   const int64_t blocks = ceil_div(units, kAppendThreads);  // of a token, at one unit per thread
-  // a few tokens are spread over the SMs; of many each block takes what it can keep on the way
-  const int per = a.T * blocks < 4 * num_sms || blocks == 1 ? 1 : (blocks == 2 || blocks == 4 ? 2 : 3);
+  // a few tokens are spread over the SMs; of many each thread takes two units (4096 tokens of 32 + 2 x
+  // 32 heads in bf16: 35.6 us against 41.5 with one; three are 35.1 in 16 bits, but in fp32, where
+  // two take 19.9 us for 2047 tokens of 64 + 2 x 8 heads, 22.9)
+  const int per = a.T * blocks < 8 * num_sms || blocks == 1 ? 1 : 2;
   const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>(ceil_div(blocks, per)));
-  auto kernel = per == 1 ? kv_append_kernel<IN, CACHE, 1>
-                         : (per == 2 ? kv_append_kernel<IN, CACHE, 2> : kv_append_kernel<IN, CACHE, 3>);
+  auto kernel = per == 1 ? kv_append_kernel<IN, CACHE, 1> : kv_append_kernel<IN, CACHE, 2>;
   return launch_early(kernel, grid, kAppendThreads, 0, s, launches, a);
 }
 

@@ -11,6 +11,13 @@
 // per row serves both forms. The maximum is taken of the bit patterns of |h w|, which
 // order as the values do and put NaN above everything: a row that holds a NaN or an
 // infinity has a NaN scale.
+//
+// What bounds it: the rows' bytes, each read and written once (x, r, r' and y; 1 GB for 16384 x
+// 8192 in bf16 with a residual). A row stays in registers between its statistic and its output,
+// and the next row's loads are issued before the reduction, so that two blocks an SM keep loads
+// on the way while both wait at a barrier: 174 us, 6.2 TB/s of the 6.55 of a copy (186 us with
+// the loads after the output; 196 us with three rows ahead in a shared-memory ring, whose
+// traffic costs more than its depth gives). One row of 4096 takes 2.7 us in a captured graph.
 #include "decode_kernels.h"
 
 #include <algorithm>
