@@ -174,33 +174,137 @@ __global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) no
   }
 }
 
-// One row per block and turn, one or more scalars per thread: any K, stride and alignment.
-// h stays in shared memory between the two uses of it.
-__global__ void __launch_bounds__(1024) norm_any_kernel(NormArgs a) {
-  extern __shared__ float h_row[];
+// Rows of any length and alignment: E pieces of VEC values per thread and turn, loaded together
+// (VEC = 1 for odd rows, 2 for even ones, 8 for aligned rows beyond norm_kernel's). A row of one
+// turn stays in registers; of a longer one (LONG) h w waits in shared memory, where each thread
+// finds its own again. The types are told apart once per turn and tensor.
+template <int TYPE, int VEC, int E>
+__device__ __forceinline__ void load_pieces(const void* row, int first, int step, int pieces, float (&v)[E][VEC]) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int at = first + i * step;
+    if (at >= pieces) continue;
+    if constexpr (VEC == 8) {
+      Raw8<TYPE> raw;
+      raw.load(row, 8 * static_cast<int64_t>(at));
+      raw.to_float(v[i]);
+    } else if constexpr (TYPE == kTypeF32) {
+      if constexpr (VEC == 2) {
+        const float2 f = static_cast<const float2*>(row)[at];
+        v[i][0] = f.x;
+        v[i][1] = f.y;
+      } else {
+        v[i][0] = static_cast<const float*>(row)[at];
+      }
+    } else if constexpr (VEC == 2) {
+      const float2 f = unpack16(static_cast<const uint32_t*>(row)[at], TYPE);
+      v[i][0] = f.x;
+      v[i][1] = f.y;
+    } else {
+      const uint32_t h = static_cast<const uint16_t*>(row)[at];
+      v[i][0] = TYPE == kTypeBf16 ? __uint_as_float(h << 16) : bits_f16(h);
+    }
+  }
+}
+template <int VEC, int E>
+__device__ __forceinline__ void load_pieces(const void* row, int type, int first, int step, int pieces, float (&v)[E][VEC]) {
+  if (type == kTypeF32)
+    load_pieces<kTypeF32>(row, first, step, pieces, v);
+  else if (type == kTypeBf16)
+    load_pieces<kTypeBf16>(row, first, step, pieces, v);
+  else
+    load_pieces<kTypeF16>(row, first, step, pieces, v);
+}
+template <int TYPE, int VEC, int E>
+__device__ __forceinline__ void store_pieces(void* row, int first, int step, int pieces, const float (&v)[E][VEC]) {
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int at = first + i * step;
+    if (at >= pieces) continue;
+    if constexpr (VEC == 8)
+      store8_as<TYPE>(row, 8 * static_cast<int64_t>(at), v[i]);
+    else if constexpr (VEC == 1)
+      store_one(row, at, TYPE, v[i][0]);
+    else if constexpr (TYPE == kTypeF32)
+      static_cast<float2*>(row)[at] = make_float2(v[i][0], v[i][1]);
+    else if constexpr (TYPE == kTypeE4m3)
+      static_cast<uint16_t*>(row)[at] = static_cast<uint16_t>(pack_e4m3(v[i][0], v[i][1]));
+    else
+      static_cast<uint32_t*>(row)[at] = pack16(v[i][0], v[i][1], TYPE);
+  }
+}
+template <int VEC, int E>
+__device__ __forceinline__ void store_pieces(void* row, int type, int first, int step, int pieces, const float (&v)[E][VEC]) {
+  switch (type) {
+    case kTypeF32: store_pieces<kTypeF32>(row, first, step, pieces, v); break;
+    case kTypeBf16: store_pieces<kTypeBf16>(row, first, step, pieces, v); break;
+    case kTypeF16: store_pieces<kTypeF16>(row, first, step, pieces, v); break;
+    default: store_pieces<kTypeE4m3>(row, first, step, pieces, v);
+  }
+}
+__device__ __forceinline__ const void* row_at(const void* p, int64_t values, int type) {
+  return static_cast<const uint8_t*>(p) + values * type_bytes(type);
+}
+
+constexpr int any_threads(int e) { return e == 4 ? 128 : 1024; }              // of a block, at most
+constexpr int any_blocks(int vec, int e) { return e == 4 ? 12 / vec + 2 * (vec - 1) : 1; }  // of that size an SM
+template <int VEC, int E, bool LONG>
+__global__ void __launch_bounds__(any_threads(E), any_blocks(VEC, E)) norm_any_kernel(NormArgs a) {
+  extern __shared__ float h_row[];  // LONG only
   __shared__ RowStat parts[2][32];
   int turn = 0;
+  const int tid = threadIdx.x, step = blockDim.x, pieces = static_cast<int>(a.K / VEC), span = E * step;
+  const bool codes = a.out_type == kTypeE4m3;
   wait_for_previous();
   start_next();
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+    const void* x = row_at(a.X, m * a.x_stride, a.x_type);
+    const void* r = row_at(a.residual, m * a.r_stride, a.r_type);
+    void* ro = const_cast<void*>(row_at(a.residual_out, m * a.ro_stride, a.r_type));
+    void* out = const_cast<void*>(row_at(a.out, m * a.K, a.out_type));
+    float h[E][VEC];
     RowStat st{0.0f, 0u};
-    for (int64_t k = threadIdx.x; k < a.K; k += blockDim.x) {
-      float h = load_one(a.X, m * a.x_stride + k, a.x_type);
+    for (int base = 0; base < pieces; base += span) {
+      const int first = base + tid;
+      float w[E][VEC];
+      load_pieces(x, a.x_type, first, step, pieces, h);
       if (a.residual) {
-        h = __fadd_rn(h, load_one(a.residual, m * a.r_stride + k, a.r_type));
-        store_one(a.residual_out, m * a.ro_stride + k, a.r_type, h);
+        load_pieces(r, a.r_type, first, step, pieces, w);
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) h[i][k] = __fadd_rn(h[i][k], w[i][k]);
+        store_pieces(ro, a.r_type, first, step, pieces, h);
       }
-      const float hw = __fmul_rn(h, load_one(a.weight, k, a.w_type));
-      h_row[k] = hw;
-      st = join(st, {__fmul_rn(h, h), __float_as_uint(hw) & 0x7FFFFFFFu});
+      load_pieces(a.weight, a.w_type, first, step, pieces, w);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if (first + i * step >= pieces) continue;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          st.ss = __fmaf_rn(h[i][k], h[i][k], st.ss);
+          h[i][k] = __fmul_rn(h[i][k], w[i][k]);
+          if (codes) st.peak = max(st.peak, __float_as_uint(h[i][k]) & 0x7FFFFFFFu);
+          if (LONG) h_row[((base + i * step) * VEC) + k * step + tid] = h[i][k];
+        }
+      }
     }
     st = block_join(warp_join(st), parts, turn);
     const float factor = row_factor(st.ss, a.K, a.eps);
-    const float scale = a.out_type == kTypeE4m3 ? row_scale(st.peak, factor) : 1.0f;
-    if (a.out_type == kTypeE4m3 && threadIdx.x == 0) a.out_scales[m] = scale;
-    for (int64_t k = threadIdx.x; k < a.K; k += blockDim.x) {  // each thread's own h
-      const float y = __fmul_rn(h_row[k], factor);
-      store_one(a.out, m * a.K + k, a.out_type, a.out_type == kTypeE4m3 ? __fdiv_rn(y, scale) : y);
+    const float scale = codes ? row_scale(st.peak, factor) : 1.0f;
+    if (codes && tid == 0) a.out_scales[m] = scale;
+    for (int base = 0; base < pieces; base += span) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if (base + tid + i * step >= pieces) continue;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          if (LONG) h[i][k] = h_row[((base + i * step) * VEC) + k * step + tid];
+          h[i][k] = __fmul_rn(h[i][k], factor);
+          if (codes) h[i][k] = __fdiv_rn(h[i][k], scale);
+        }
+      }
+      store_pieces(out, a.out_type, base + tid, step, pieces, h);
     }
   }
 }
@@ -241,27 +345,53 @@ cudaError_t launch_norm_residual(const NormArgs& a, int num_sms, cudaStream_t s,
   }
 }
 
-bool rows_aligned(const void* p, int64_t stride, int type) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride * type_bytes(type) % 16 == 0;
+// Whether the rows of every tensor start at whole pieces of `vec` values.
+bool rows_aligned(const NormArgs& a, int vec) {
+  auto whole = [&](const void* p, int64_t stride, int type) {
+    const int64_t bytes = std::min(16, vec * type_bytes(type));  // of a load or store
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (a.M == 1 || stride * type_bytes(type) % bytes == 0);
+  };
+  return a.K % vec == 0 && whole(a.X, a.x_stride, a.x_type) && whole(a.weight, 0, a.w_type) && whole(a.out, a.K, a.out_type) &&
+         (!a.residual || (whole(a.residual, a.r_stride, a.r_type) && whole(a.residual_out, a.ro_stride, a.r_type)));
+}
+
+template <int VEC, int E, bool LONG>
+cudaError_t launch_any(const NormArgs& a, int num_sms, cudaStream_t s, int* launches) {
+  const int64_t pieces = a.K / VEC;
+  const int threads = LONG ? 1024 : static_cast<int>(ceil_div(ceil_div(pieces, E), 32) * 32);
+  // of a long row every turn has its own places, the last one's whether or not they are all used
+  const size_t smem = LONG ? static_cast<size_t>(ceil_div(pieces, threads) * threads * VEC) * 4 : 0;
+  if (LONG) {
+    static unsigned long long done = 0;
+    const cudaError_t e = set_smem_limit_once(norm_any_kernel<VEC, E, LONG>, static_cast<int>(kNormMaxK * 4), &done);
+    if (e != cudaSuccess) return e;
+  }
+  const int resident = LONG ? 1 : std::min(32, any_threads(E) * any_blocks(VEC, E) / threads);  // blocks an SM
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(a.M, static_cast<int64_t>(resident) * num_sms));
+  return launch_early(norm_any_kernel<VEC, E, LONG>, dim3(blocks), threads, smem, s, launches, a);
+}
+
+template <int VEC>
+cudaError_t launch_any_length(const NormArgs& a, int num_sms, cudaStream_t s, int* launches) {
+  const int64_t pieces = a.K / VEC;
+  if constexpr (VEC < 8) {
+    if (pieces <= 4 * 128) return launch_any<VEC, 4, false>(a, num_sms, s, launches);
+    if (pieces <= (16 / VEC) * 1024) return launch_any<VEC, 16 / VEC, false>(a, num_sms, s, launches);
+  }
+  return launch_any<VEC, 16 / VEC, true>(a, num_sms, s, launches);
 }
 
 }  // namespace
 
 cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s, int* launches) {
-  // the vector form: 16-byte vectors everywhere (8 bytes of an e4m3 output) and a row in registers
-  if (a.K % 8 == 0 && a.K <= 16384 && rows_aligned(a.X, a.x_stride, a.x_type) && rows_aligned(a.weight, 0, a.w_type) &&
-      (a.out_type == kTypeE4m3 ? (reinterpret_cast<uintptr_t>(a.out) & 7u) == 0 : rows_aligned(a.out, a.K, a.out_type)) &&
-      (!a.residual || (rows_aligned(a.residual, a.r_stride, a.r_type) && rows_aligned(a.residual_out, a.ro_stride, a.r_type)))) {
+  if (rows_aligned(a, 8)) {
+    if (a.K > 16384) return launch_any_length<8>(a, num_sms, s, launches);
     if (a.x_type == kTypeF32) return launch_norm_residual<kTypeF32>(a, num_sms, s, launches);
     if (a.x_type == kTypeF16) return launch_norm_residual<kTypeF16>(a, num_sms, s, launches);
     return launch_norm_residual<kTypeBf16>(a, num_sms, s, launches);
   }
-  const int threads = static_cast<int>(std::min<int64_t>(1024, ceil_div(a.K, 32) * 32));
-  static unsigned long long done = 0;
-  const cudaError_t e = set_smem_limit_once(norm_any_kernel, static_cast<int>(kNormMaxK * 4), &done);
-  if (e != cudaSuccess) return e;
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(a.M, 8 * num_sms));
-  return launch_early(norm_any_kernel, dim3(blocks), threads, static_cast<size_t>(a.K) * 4, s, launches, a);
+  if (rows_aligned(a, 2)) return launch_any_length<2>(a, num_sms, s, launches);
+  return launch_any_length<1>(a, num_sms, s, launches);
 }
 
 }  // namespace awq
