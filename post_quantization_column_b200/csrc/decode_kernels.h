@@ -131,6 +131,25 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, int type) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// v / scale as a product with 1 / scale, where that is finite (within 2^-23 of the quotient, a
+// quarter of a millionth of an e4m3 step, for an eighth of a division's instructions).
+struct Divisor {
+  float scale, inverse;
+  bool product;
+  __device__ __forceinline__ explicit Divisor(float s) : scale(s), inverse(1.0f / s) {
+    product = fabsf(inverse) <= 3.402823466e38f;
+  }
+  template <int N>
+  __device__ __forceinline__ void divide(float (&v)[N]) const {
+    if (product) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = __fmul_rn(v[k], inverse);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = __fdiv_rn(v[k], scale);
+    }
+  }
+};
 // Two values rounded to e4m3 (finite values beyond +-448 saturate; NaN stays NaN).
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);

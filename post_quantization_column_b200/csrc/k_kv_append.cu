@@ -142,12 +142,9 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(AppendArgs
     } else if (row >= 0) {
       const int hh = vh < 0 ? kh : vh;
       if constexpr (CACHE == kTypeE4m3) {
-        const float scale = (vh < 0 ? c.k_scale : c.v_scale)[hh];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          x[k] = __fdiv_rn(x[k], scale);
-          y[k] = __fdiv_rn(y[k], scale);
-        }
+        const Divisor scale((vh < 0 ? c.k_scale : c.v_scale)[hh]);
+        scale.divide(x);
+        scale.divide(y);
       }
       uint8_t* dst = static_cast<uint8_t*>(vh < 0 ? c.k : c.v) + row + static_cast<uint64_t>(static_cast<uint32_t>(hh) * a.cache_head32) * 32u;
       store8_as<CACHE>(dst, d0, x);

@@ -18,51 +18,12 @@
 // on the way while both wait at a barrier: 174 us, 6.2 TB/s of the 6.55 of a copy (186 us with
 // the loads after the output; 196 us with three rows ahead in a shared-memory ring, whose
 // traffic costs more than its depth gives). One row of 4096 takes 2.7 us in a captured graph.
-#include "decode_kernels.h"
+#include "rmsnorm.cuh"
 
 #include <algorithm>
 
 namespace awq {
 namespace {
-
-struct RowStat {
-  float ss;
-  uint32_t peak;  // bits of max |h w|
-};
-
-__device__ __forceinline__ RowStat join(RowStat a, RowStat b) {
-  a.ss = __fadd_rn(a.ss, b.ss);
-  a.peak = max(a.peak, b.peak);
-  return a;
-}
-
-__device__ __forceinline__ RowStat warp_join(RowStat a) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    a = join(a, {__shfl_xor_sync(~0u, a.ss, o), __shfl_xor_sync(~0u, a.peak, o)});
-  return a;
-}
-
-// The statistic of a row whose parts the block's warps hold, in every thread. Rows take turns
-// between two sets of slots, so that one barrier a row is enough.
-__device__ __forceinline__ RowStat block_join(RowStat a, RowStat (*shared)[32], int& turn) {
-  const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
-  if (warps == 1) return a;
-  RowStat* slots = shared[turn];
-  turn ^= 1;
-  if (lane == 0) slots[threadIdx.x / 32] = a;
-  __syncthreads();
-  return warp_join(lane < warps ? slots[lane] : RowStat{0.0f, 0u});
-}
-
-__device__ __forceinline__ float row_factor(float ss, int64_t K, float eps) {
-  return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(K)), eps)));
-}
-
-__device__ __forceinline__ float row_scale(uint32_t peak, float factor) {
-  const float scale = __fdiv_rn(__fmul_rn(__uint_as_float(peak), factor), kE4m3Max);
-  return scale == 0.0f ? 1.0f : scale;
-}
 
 // Vector v of the weight.
 __device__ __forceinline__ void load_weight(const NormArgs& a, int v, float (&w)[8]) {
@@ -88,14 +49,15 @@ template <int VPT>
 __device__ __forceinline__ void write_row(const NormArgs& a, int64_t m, int lane, int width, int vecs, RowStat st, float (&h)[VPT][8]) {
   const float factor = row_factor(st.ss, a.K, a.eps);
   if (a.out_type == kTypeE4m3) {
-    const float scale = row_scale(st.peak, factor);
-    if (lane == 0) a.out_scales[m] = scale;
+    const Divisor scale(row_scale(st.peak, factor));
+    if (lane == 0) a.out_scales[m] = scale.scale;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = lane + i * width;
       if (v >= vecs) continue;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) h[i][k] = __fdiv_rn(__fmul_rn(h[i][k], factor), scale);
+      for (int k = 0; k < 8; ++k) h[i][k] = __fmul_rn(h[i][k], factor);
+      scale.divide(h[i]);
       store8_as<kTypeE4m3>(a.out, m * a.K + 8 * v, h[i]);
     }
   } else {
@@ -242,9 +204,6 @@ __device__ __forceinline__ void store_pieces(void* row, int type, int first, int
     default: store_pieces<kTypeE4m3>(row, first, step, pieces, v);
   }
 }
-__device__ __forceinline__ const void* row_at(const void* p, int64_t values, int type) {
-  return static_cast<const uint8_t*>(p) + values * type_bytes(type);
-}
 
 constexpr int any_threads(int e) { return e == 4 ? 128 : 1024; }              // of a block, at most
 constexpr int any_blocks(int vec, int e) { return e == 4 ? 12 / vec + 2 * (vec - 1) : 1; }  // of that size an SM
@@ -291,8 +250,8 @@ __global__ void __launch_bounds__(any_threads(E), any_blocks(VEC, E)) norm_any_k
     }
     st = block_join(warp_join(st), parts, turn);
     const float factor = row_factor(st.ss, a.K, a.eps);
-    const float scale = codes ? row_scale(st.peak, factor) : 1.0f;
-    if (codes && tid == 0) a.out_scales[m] = scale;
+    const Divisor scale(codes ? row_scale(st.peak, factor) : 1.0f);
+    if (codes && tid == 0) a.out_scales[m] = scale.scale;
     for (int base = 0; base < pieces; base += span) {
 #pragma unroll
       for (int i = 0; i < E; ++i) {
@@ -301,8 +260,8 @@ __global__ void __launch_bounds__(any_threads(E), any_blocks(VEC, E)) norm_any_k
         for (int k = 0; k < VEC; ++k) {
           if (LONG) h[i][k] = h_row[((base + i * step) * VEC) + k * step + tid];
           h[i][k] = __fmul_rn(h[i][k], factor);
-          if (codes) h[i][k] = __fdiv_rn(h[i][k], scale);
         }
+        if (codes) scale.divide(h[i]);
       }
       store_pieces(out, a.out_type, base + tid, step, pieces, h);
     }
@@ -355,6 +314,15 @@ bool rows_aligned(const NormArgs& a, int vec) {
          (!a.residual || (whole(a.residual, a.r_stride, a.r_type) && whole(a.residual_out, a.ro_stride, a.r_type)));
 }
 
+// Whether row m of every tensor starts (m K) mod 8 values beyond a whole vector.
+bool rows_shifted(const NormArgs& a) {
+  auto like = [&](const void* p, int64_t stride, int type) {
+    return reinterpret_cast<uintptr_t>(p) % std::min(16, 8 * type_bytes(type)) == 0 && (a.M == 1 || (stride - a.K) % 8 == 0);
+  };
+  return like(a.X, a.x_stride, a.x_type) && like(a.out, a.K, a.out_type) &&
+         (!a.residual || (like(a.residual, a.r_stride, a.r_type) && like(a.residual_out, a.ro_stride, a.r_type)));
+}
+
 template <int VEC, int E, bool LONG>
 cudaError_t launch_any(const NormArgs& a, int num_sms, cudaStream_t s, int* launches) {
   const int64_t pieces = a.K / VEC;
@@ -390,6 +358,7 @@ cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s, int*
     if (a.x_type == kTypeF16) return launch_norm_residual<kTypeF16>(a, num_sms, s, launches);
     return launch_norm_residual<kTypeBf16>(a, num_sms, s, launches);
   }
+  if (rows_shifted(a) && a.K >= 64 && a.K < 16384) return launch_rms_norm_shifted(a, num_sms, s, launches);
   if (rows_aligned(a, 2)) return launch_any_length<2>(a, num_sms, s, launches);
   return launch_any_length<1>(a, num_sms, s, launches);
 }

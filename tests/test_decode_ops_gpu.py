@@ -6,10 +6,12 @@ an output type relative to the value (tiny(t) / 2 absolute below its normal rang
 * RMS norm: h is one fp32 addition (u); sum h^2 adds at most K / 32 terms one after the other in
   a thread and fewer than 64 partial sums, each product and addition rounded once, and the square
   root halves the relative error: (K / 32 + 66) u / 2; h w, the quotient, the root, the
-  reciprocal and the last product add fewer than 8 roundings. Then eta of the output.
+  reciprocal, the last product and the quotient by a scale add fewer than 10 roundings. Then eta of
+  the output.
 * Rotation: the fraction of a turn is rounded to fp32 (at most 2^-26 turns = 2 pi 2^-26), sine
   and cosine of it are within 2 ulp (2^-23), the magnitude and the two products and the sum add
-  3 roundings: a pair (x, y) comes within (|x| + |y|) |m| (2 pi 2^-26 + 2^-23 + 3 u), plus eta.
+  3 roundings: a pair (x, y) comes within (|x| + |y|) |m| (2 pi 2^-26 + 2^-23 + 3 u), plus eta. The
+  quotient by an e4m3 scale is a product with the rounded reciprocal: 2 u, and 1 for their product.
 * Attention: a score is an fp32 sum of D exact products: it is off by at most 2 D u scale
   sum |q k| (twice the bound of D rounded additions, since a tensor-core step may truncate),
   plus 4 u |s| for the scale in base 2; a weight is then off by that (as a factor), by the
@@ -203,7 +205,7 @@ def _check_append(q, k, v, before, caches, table, positions, freqs, out, seqs=No
     for x, old, new, scale, turn in ((k, before[0], caches[0], scales[0], True), (v, before[1], caches[1], scales[1], False)):
         ref, tol = turned(x) if turn else (_np(x), np.zeros(x.shape))
         s = np.ones(x.shape[1]) if scale is None else _np(scale)
-        ref, tol = ref / s[:, None], tol / s[:, None] + (0 if scale is None else U * np.abs(ref / s[:, None]))
+        ref, tol = ref / s[:, None], tol / s[:, None] + (0 if scale is None else 3 * U * np.abs(ref / s[:, None]))
         got, want = _np(new), _np(old)
         touched = np.zeros(want.shape[:2], dtype=bool)
         for t, (p, slot) in enumerate(at):
