@@ -49,9 +49,9 @@ __device__ __forceinline__ void store_window(void* row, int first, int K, const 
 
 // Blocks of up to 544 threads: 8192 values and a row's ends in two windows each.
 constexpr int threads_of(bool warp) { return warp ? 256 : 544; }
-constexpr int blocks_of(int vpt, bool warp) { return warp ? 2 : (vpt <= 2 ? 2 : 1); }  // of that size an SM
+constexpr int blocks_of(int vpt, bool warp, bool wide) { return warp ? 2 : (vpt + wide <= 2 ? 2 : 1); }  // of that size an SM
 template <int TX, int TR, int VPT, bool WARP>
-__global__ void __launch_bounds__(threads_of(WARP), blocks_of(VPT, WARP)) norm_shifted_kernel(NormArgs a) {
+__global__ void __launch_bounds__(threads_of(WARP), blocks_of(VPT, WARP, TX == kTypeF32 || TR == kTypeF32)) norm_shifted_kernel(NormArgs a) {
   extern __shared__ float weight[];
   __shared__ RowStat parts[2][32];
   int turn = 0;
@@ -146,7 +146,7 @@ cudaError_t launch(const NormArgs& a, int num_sms, cudaStream_t s, int* launches
   static unsigned long long done = 0;
   const cudaError_t e = set_smem_limit_once(norm_shifted_kernel<TX, TR, VPT, WARP>, 80 * 1024, &done);
   if (e != cudaSuccess) return e;
-  const int64_t resident = std::min<int64_t>(std::min(32, threads_of(WARP) * blocks_of(VPT, WARP) / threads), 220 * 1024 / (smem + 2048));
+  const int64_t resident = std::min<int64_t>(std::min(32, threads_of(WARP) * blocks_of(VPT, WARP, TX == kTypeF32 || TR == kTypeF32) / threads), 220 * 1024 / (smem + 2048));
   const int64_t rows = WARP ? threads / 32 : 1;
   const unsigned blocks = static_cast<unsigned>(std::min(ceil_div(a.M, rows), resident * num_sms));
   return launch_early(norm_shifted_kernel<TX, TR, VPT, WARP>, dim3(blocks), threads, smem, s, launches, a);
