@@ -51,7 +51,16 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 3 * 148;  // three CTAs on each of a B200's SMs
 constexpr int kWhole = 4;           // units of the longest segment that is not cut
-constexpr int kLong = 40;           // units a CTA from which heads lie side by side
+// Over short rows (kShort), the four warps of a CTA can take four heads of the same tokens instead of
+// four parts of one head's tokens (Geometry::side). That pays
+// - in batches where no sequence has more than one unit, with kMany units a CTA or more: a
+//   segment's end, where the warps meet, then comes once for four heads (243 ragged sequences up
+//   to 86, 32 e4m3 heads: 49 against 68 us);
+// - in long runs where the heads lie side by side in memory, with kLong units a CTA or
+//   more: what is read at one time lies together (e4m3, D = 128, 8 heads: 55 x 8192 tokens 161
+//   against 165 us, 55 x 4096 91 against 88; 32 heads, 32 ragged sequences up to 8192: 195 against
+//   210 us). Units are a quarter as deep there and leave four heads' partial sums at a run's ends.
+constexpr int kMany = 2, kLong = 40;
 
 template <int D, int TYPE, int NB>
 struct Tile {
@@ -167,7 +176,8 @@ struct Geometry {
   int cap;           // tokens a table row can name
   int heads_per;     // Hq / Hkv
   int hgroups;       // blocks of query heads per key-value head
-  int side;          // key-value heads that may lie side by side in a CTA: 1, 2 or 4, of kWarps / side warps each
+  int side;          // key-value heads that may go side by side in a CTA: 1, 2 or 4, of kWarps / side warps each
+  int adjacent;      // the heads of a token lie side by side in memory
   int64_t ctas;
   int by_segment;    // the joins are listed by segment
   int64_t listed;
@@ -235,7 +245,10 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   };
   int side = 1;
   count_units(kTok * kWarps);
-  if (T_::kShort && geo.side > 1 && total * c.heads * geo.hgroups >= kLong * geo.ctas) {
+  const bool snap = longest <= kWhole;
+  const int64_t all = total * c.heads * geo.hgroups;
+  if (T_::kShort && geo.side > 1 &&
+      (longest <= 1 ? all >= kMany * geo.ctas : geo.adjacent && all >= kLong * geo.ctas)) {
     side = geo.side;
     __syncthreads();  // the sums have been read
     count_units(kTok * kWarps / side);
@@ -246,7 +259,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   // No run is empty: with fewer units than CTAs the later CTAs have none. Where segments are short a
   // run begins and ends with one instead (and may be empty): a join takes longer than kWhole units.
   const int64_t units = total * HH, C = min(geo.ctas, units);
-  const bool snap = longest <= kWhole;
   int64_t ends_at[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -422,66 +434,77 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
   float acc[NB][S][4];            // O^T: per 16-dim tile, (dim, dim + 1) x (heads 2t, 2t + 1)
   float ls[NB][2];                // l of heads 2t, 2t + 1
   float m[NB][2], sc[NB][2];      // the maximum in use, lowered by kBias; the factor of the products, base 2
-  bool bad = false, fresh = true;
-  for (int i = 0; i < n; ++i) {
-    if (fresh) {  // a segment of the run begins
-      fresh = false;
-      bad = a.lengths[cc.b] > geo.cap;
-      const int kvh = cc.kg * side + head_of, hb = cc.hg * T_::kHeads;
-      const float k_scale = TYPE == kTypeE4m3 ? c.k_scale[kvh] : 1.0f;
+  bool bad = false;
+  auto load_queries = [&](const Cursor& at) {
+    const int kvh = at.kg * side + head_of, hb = at.hg * T_::kHeads;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int h = hb + nb * 8 + g;
-        const bool live = h < geo.heads_per;
-        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;  // the factor of the scores is not negative
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) + cc.b * a.q_sb +
-                            static_cast<int64_t>(kvh * geo.heads_per + (live ? h : 0)) * a.q_sh;
+    for (int nb = 0; nb < NB; ++nb) {
+      const int h = hb + nb * 8 + g;
+      const bool live = h < geo.heads_per;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) + at.b * a.q_sb +
+                          static_cast<int64_t>(kvh * geo.heads_per + (live ? h : 0)) * a.q_sh;
 #pragma unroll
-        for (int st = 0; st < S; ++st) {
-          // dims of step st: 4 elements of the lane's piece st / PER
-          constexpr int PER = KB / (4 * ES);  // steps that a piece serves
-          const int d = (st / PER) * (4 * KB / ES) + (KB / ES) * t + 4 * (st % PER);
-          const uint2 w = live ? *reinterpret_cast<const uint2*>(q + d) : make_uint2(0u, 0u);
-          qf[nb][st][0] = w.x ^ flip;
-          qf[nb][st][1] = w.y ^ flip;
-        }
-        float up = 1.0f;
-        if (TYPE == kTypeE4m3 && a.q_type == kTypeBf16) {
-          // the products run in fp16: bf16 queries are brought to [1, 2) by a power of two
-          float peak = 0.0f;
-#pragma unroll
-          for (int st = 0; st < S; ++st)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float2 f = unpack16(qf[nb][st][x], kTypeBf16);
-              peak = fmaxf(peak, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-          peak = fmaxf(peak, __shfl_xor_sync(~0u, peak, 1));
-          peak = fmaxf(peak, __shfl_xor_sync(~0u, peak, 2));
-          const uint32_t e = __float_as_uint(peak) & 0x7F800000u;
-          float down = 1.0f;
-          if (e > 0x01000000u && e < 0x7E000000u) {
-            up = __uint_as_float(e);
-            down = __uint_as_float(0x7F000000u - e);
-          }
-#pragma unroll
-          for (int st = 0; st < S; ++st)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float2 f = unpack16(qf[nb][st][x], kTypeBf16);
-              qf[nb][st][x] = pack16(f.x * down, f.y * down, kTypeF16);
-            }
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          sc[nb][x] = fabsf(a.scale * 1.4426950408889634f) * k_scale * __shfl_sync(~0u, up, (2 * t + x) * 4);
-          m[nb][x] = kNoMax;
-        }
-#pragma unroll
-        for (int st = 0; st < S; ++st) acc[nb][st][0] = acc[nb][st][1] = acc[nb][st][2] = acc[nb][st][3] = 0.0f;
-        ls[nb][0] = ls[nb][1] = 0.0f;
+      for (int st = 0; st < S; ++st) {
+        // dims of step st: 4 elements of the lane's piece st / PER
+        constexpr int PER = KB / (4 * ES);  // steps that a piece serves
+        const int d = (st / PER) * (4 * KB / ES) + (KB / ES) * t + 4 * (st % PER);
+        qf[nb][st][0] = qf[nb][st][1] = 0u;
+        if (live) asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(qf[nb][st][0]), "=r"(qf[nb][st][1]) : "l"(q + d));
       }
     }
+  };
+  auto begin_segment = [&]() {
+    bad = a.lengths[cc.b] > geo.cap;
+    const float k_scale = TYPE == kTypeE4m3 ? c.k_scale[cc.kg * side + head_of] : 1.0f;
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;  // the factor of the scores is not negative
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int st = 0; st < S; ++st) {
+        qf[nb][st][0] ^= flip;
+        qf[nb][st][1] ^= flip;
+      }
+      float up = 1.0f;
+      if (TYPE == kTypeE4m3 && a.q_type == kTypeBf16) {
+        // the products run in fp16: bf16 queries are brought to [1, 2) by a power of two
+        float peak = 0.0f;
+#pragma unroll
+        for (int st = 0; st < S; ++st)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 f = unpack16(qf[nb][st][x], kTypeBf16);
+            peak = fmaxf(peak, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        peak = fmaxf(peak, __shfl_xor_sync(~0u, peak, 1));
+        peak = fmaxf(peak, __shfl_xor_sync(~0u, peak, 2));
+        const uint32_t e = __float_as_uint(peak) & 0x7F800000u;
+        float down = 1.0f;
+        if (e > 0x01000000u && e < 0x7E000000u) {
+          up = __uint_as_float(e);
+          down = __uint_as_float(0x7F000000u - e);
+        }
+#pragma unroll
+        for (int st = 0; st < S; ++st)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 f = unpack16(qf[nb][st][x], kTypeBf16);
+            qf[nb][st][x] = pack16(f.x * down, f.y * down, kTypeF16);
+          }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        sc[nb][x] = fabsf(a.scale * 1.4426950408889634f) * k_scale * __shfl_sync(~0u, up, (2 * t + x) * 4);
+        m[nb][x] = kNoMax;
+      }
+#pragma unroll
+      for (int st = 0; st < S; ++st) acc[nb][st][0] = acc[nb][st][1] = acc[nb][st][2] = acc[nb][st][3] = 0.0f;
+      ls[nb][0] = ls[nb][1] = 0.0f;
+    }
+  };
+  load_queries(cc);
+  begin_segment();
+  for (int i = 0; i < n; ++i) {
+    const bool ends = (cc.blk + 1) * unit >= cc.len, last = i + 1 == n;
     bad = bad || bad_now;
     const int tok0 = cc.blk * unit + tok_of;
     // one block and one group of heads: two chains of products, for their latency
@@ -525,6 +548,9 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
           for (int x = 0; x < 4; ++x) s[k][nb][x] = CHAINS == 2 ? s2[0][k][nb][x] + s2[CHAINS - 1][k][nb][x] : s2[0][k][nb][x];
       }
     }
+    Cursor next = cc;
+    if (!last) advance(next);
+    if (ends && !last) load_queries(next);  // these have been used
     place();
     load_keys();
     {
@@ -619,7 +645,6 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
     bad_now = bad_tile;
     look_up();
 
-    const bool ends = (cc.blk + 1) * unit >= cc.len, last = i + 1 == n;
     if (ends || last) {
       // ---- the four warps meet: factors to the common maximum, then one sum per head and dim
 #pragma unroll
@@ -641,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
       const int live = min(T_::kHeads, geo.heads_per - hb);
       if (any_bad && tid == 0 && a.status) *a.status = 1;
       const bool begins = seg0 >= u0;
-      if (tid < SUB && (geo.by_segment ? begins && tid < side : last)) {
+      if (tid < kWarps && (geo.by_segment ? begins && tid < side : last && tid < SUB)) {
         const int hh = (cc.kg * side + tid) * geo.hgroups + cc.hg;
         int pieces = 0;
         if (begins && !ends && tid < side)
@@ -701,9 +726,9 @@ __global__ void __launch_bounds__(kThreads, Tile<D, TYPE, NB>::kCtas)
         }
       }
       __syncthreads();
-      fresh = true;
     }
-    if (!last) advance(cc);
+    cc = next;
+    if (ends && !last) begin_segment();
   }
 }
 
@@ -765,17 +790,6 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(PagedAttn
       make_uint2(pack16(o.x * x, o.y * x, a.q_type), pack16(o.z * x, o.w * x, a.q_type));
 }
 
-// Where the heads of a token lie side by side and rows are short, the four warps of a CTA can take
-// four heads of the same tokens instead of four runs of tokens of one head, so that what is read
-// at one time lies together in memory. It pays from some 40 units a CTA on (kLong; e4m3, D = 128,
-// 8 heads: 55 x 8192 tokens 161 against 165 us, 55 x 4096 91 against 88; 32 heads, 32 ragged
-// sequences up to 8192: 195 against 210 us), since the units are a quarter as deep and leave four
-// heads' partial sums where they cross runs.
-int heads_side_by_side(const PagedCache& c) {
-  if (c.head_dim * type_bytes(c.type) > 128 || c.head_stride >= c.slot_stride) return 1;
-  return c.heads % 4 == 0 ? 4 : (c.heads % 2 == 0 ? 2 : 1);
-}
-
 // Blocks of 8 query heads that share a pass over the cache: two where a group has more than 8 and
 // the registers hold both. Larger groups read the cache again, from L2 for the most part.
 int head_blocks(int Hq, int Hkv, int D) { return Hq / Hkv > 8 && D <= 128 ? 2 : 1; }
@@ -787,7 +801,8 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t s, int* lau
   geo.cap = static_cast<int>(std::min<int64_t>(a.c.max_pages * a.c.page_size, INT32_MAX - 1024));
   geo.heads_per = a.Hq / a.c.heads;
   geo.hgroups = static_cast<int>(ceil_div(geo.heads_per, T_::kHeads));
-  geo.side = heads_side_by_side(a.c);
+  geo.side = a.c.heads % 4 == 0 ? 4 : (a.c.heads % 2 == 0 ? 2 : 1);
+  geo.adjacent = a.c.head_stride < a.c.slot_stride;
   const int unit = T_::kTok * kWarps;  // tokens of a unit of one head
   const int64_t segments = a.B * a.c.heads * geo.hgroups;
   geo.ctas = std::min<int64_t>(std::min(kMaxCtas, T_::kCtas * num_sms), segments * ceil_div(geo.cap, unit));

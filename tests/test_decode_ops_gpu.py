@@ -402,6 +402,25 @@ def test_attention_long_batches_of_short_rows(lens, Hq, H, Dh, page, qt, cache):
         assert torch.allclose(alone[0].float(), out[b].float(), atol=2e-3, rtol=2e-2), b
 
 
+@pytest.mark.parametrize("order", ["pshd", "phsd", "hpsd"])
+@pytest.mark.parametrize("qt,cache,Dh,Hq,H,page", [(F16, F16, 64, 32, 32, 16), (BF16, E4M3, 128, 32, 8, 8), (F16, E4M3, 64, 20, 10, 24), (BF16, E4M3, 128, 90, 9, 16)])
+@pytest.mark.parametrize("width", [None, 4096])
+def test_attention_many_short_sequences_over_short_rows(order, qt, cache, Dh, Hq, H, page, width):
+    """No sequence longer than one unit of work, and many of them: the heads of a token go side by
+    side where they go in fours or twos. `width`: the tokens that a row of the table has room for."""
+    unit = 32768 // (2 * Dh * (2 if cache == F16 else 1))
+    lens = [min(n, unit) for n in (0, 1, 15, 16, 17, 31, 33, unit // 4, unit // 4 + 1, unit // 2 - 1, unit // 2 + 1, unit - 1, unit, 0)] * 20
+    q, kc, vc, table, lt, (ks, vs) = _attn_case(lens, Hq, H, Dh, page, qt, cache, order, seed=Hq)
+    if width is not None:
+        table = torch.nn.functional.pad(table, (0, width // page - table.shape[1]), value=-1)
+    out = awq.paged_attention(q, kc, vc, table, lt, k_scale=ks, v_scale=vs)
+    _check_attention(q, kc, vc, table, lt, out, None, ks, vs, rows=range(14))
+    for b in (50, 133, 279):
+        _check_attention(q, kc, vc, table, lt, out, None, ks, vs, rows=[b])
+    assert torch.isfinite(out.float()).all()
+    assert torch.equal(out, awq.paged_attention(q, kc, vc, table, lt, k_scale=ks, v_scale=vs))
+
+
 def test_attention_peaked_and_flat_scores():
     q, kc, vc, table, lens, _ = _attn_case([900, 130, 40], 4, 4, 128, 16, F16, F16, seed=5, spread=20.0)
     out = awq.paged_attention(q, kc, vc, table, lens)
