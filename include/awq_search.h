@@ -381,7 +381,8 @@ int awq_w4a16_dequant(const int32_t* codes, const void* steps, const void* zeros
  * contiguous holds one of these types, or AWQ_DTYPE_E4M3: out_scales[m] = max_k |y| / 448 (1
  * where that is zero) and out = e4m3(y / out_scales[m]); a row with a NaN or an infinity has
  * a NaN scale. 0 <= M < 2^31 (0 does nothing), 1 <= K <= 57344. Rows of aligned 16-byte
- * vectors (K % 8 == 0, K <= 16384) are the fast form. */
+ * vectors (K % 8 == 0, K <= 16384) are the fastest, then rows of any other length from 64 to
+ * 16384 that follow one another without a gap. */
 int awq_rms_norm(const void* X, int x_dtype, int64_t x_stride, const void* residual, int r_dtype,
                  int64_t r_stride, void* residual_out, int64_t ro_stride, const void* weight,
                  int w_dtype, int64_t M, int64_t K, float eps, void* out, int out_dtype,

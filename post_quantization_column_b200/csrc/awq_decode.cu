@@ -143,6 +143,7 @@ int awq_rms_norm_on(int device, const void* X, int x_dtype, int64_t x_stride, co
   a.out_scales = out_scales;
   a.M = M;
   a.K = K;
+  a.inverse_k = 1.0f / static_cast<float>(K);
   a.x_stride = x_stride;
   a.r_stride = r_stride;
   a.ro_stride = ro_stride;

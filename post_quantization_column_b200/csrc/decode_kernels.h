@@ -33,7 +33,7 @@ struct NormArgs {
   float* out_scales;         // [M], e4m3 output only
   int64_t M, K, x_stride, r_stride, ro_stride;
   int x_type, r_type, w_type, out_type;
-  float eps;
+  float eps, inverse_k;      // inverse_k: 1 / K
 };
 cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t s, int* launches);
 

@@ -15,9 +15,10 @@
 // What bounds it: the rows' bytes, each read and written once (x, r, r' and y; 1 GB for 16384 x
 // 8192 in bf16 with a residual). A row stays in registers between its statistic and its output,
 // and the next row's loads are issued before the reduction, so that two blocks an SM keep loads
-// on the way while both wait at a barrier: 174 us, 6.2 TB/s of the 6.55 of a copy (186 us with
-// the loads after the output; 196 us with three rows ahead in a shared-memory ring, whose
-// traffic costs more than its depth gives). One row of 4096 takes 2.7 us in a captured graph.
+// on the way while both wait at a barrier: 168 us, 6.4 TB/s of the 6.55 of a copy (12 us more with
+// the loads after the output; 22 more with three rows ahead in a shared-memory ring, whose
+// traffic costs more than its depth gives). One row of 4096 takes 2.7 us in a captured graph,
+// 100000 bf16 rows of 64 6.0 us (18 with a warp a row).
 #include "rmsnorm.cuh"
 
 #include <algorithm>
@@ -47,7 +48,7 @@ __device__ __forceinline__ void load_weight(const NormArgs& a, int v, float (&w)
 // The thread's vectors h w of row m, with the row's statistic, to the output.
 template <int VPT>
 __device__ __forceinline__ void write_row(const NormArgs& a, int64_t m, int lane, int width, int vecs, RowStat st, float (&h)[VPT][8]) {
-  const float factor = row_factor(st.ss, a.K, a.eps);
+  const float factor = row_factor(st.ss, a);
   if (a.out_type == kTypeE4m3) {
     const Divisor scale(row_scale(st.peak, factor));
     if (lane == 0) a.out_scales[m] = scale.scale;
@@ -73,17 +74,17 @@ __device__ __forceinline__ void write_row(const NormArgs& a, int64_t m, int lane
 }
 
 // Rows of aligned vectors of 8 values: the whole row lies in the registers of its threads, VPT
-// vectors each, between the reduction and the output. A row belongs to a warp (WARP, 8 rows a
-// block) or to a block; several blocks an SM load while others reduce, and the weight stays in
+// vectors each, between the reduction and the output. A row belongs to 8, 16 or 32 LANES of a warp,
+// or to a block (LANES = 0); several blocks an SM load while others reduce, and the weight stays in
 // the L1 cache, which the rows themselves pass by.
-constexpr int norm_threads(bool warp) { return warp ? 256 : 512; }  // of a block, at most
-constexpr int norm_blocks(int vpt, bool warp) { return (warp ? 2 : 1) * (vpt <= 2 ? 2 : 1); }  // of that size an SM
-template <int TX, int TR, int VPT, bool WARP>
-__global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) norm_kernel(NormArgs a) {
+constexpr int norm_threads(int lanes) { return lanes ? 256 : 512; }  // of a block, at most
+constexpr int norm_blocks(int vpt, int lanes) { return (lanes ? 2 : 1) * (vpt <= 2 ? 2 : 1); }  // of that size an SM
+template <int TX, int TR, int VPT, int LANES>
+__global__ void __launch_bounds__(norm_threads(LANES), norm_blocks(VPT, LANES)) norm_kernel(NormArgs a) {
   __shared__ RowStat parts[2][32];
   int turn = 0;
-  const int lane = WARP ? threadIdx.x % 32 : threadIdx.x, width = WARP ? 32 : blockDim.x;
-  const int rows = WARP ? blockDim.x / 32 : 1;
+  const int lane = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x, width = LANES ? LANES : blockDim.x;
+  const int rows = LANES ? blockDim.x / width : 1;
   const int vecs = static_cast<int>(a.K / 8);
   const bool codes = a.out_type == kTypeE4m3;
   wait_for_previous();
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) no
       }
     }
   };
-  int64_t m = static_cast<int64_t>(blockIdx.x) * rows + (WARP ? threadIdx.x / 32 : 0);
+  int64_t m = static_cast<int64_t>(blockIdx.x) * rows + (LANES ? threadIdx.x / width : 0);
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   if (m < a.M) load_row(m);
   for (; m < a.M; m += step) {
@@ -130,8 +131,10 @@ __global__ void __launch_bounds__(norm_threads(WARP), norm_blocks(VPT, WARP)) no
       }
     }
     if (m + step < a.M) load_row(m + step);  // on the way during the reduction and the output
-    st = warp_join(st);
-    if (!WARP) st = block_join(st, parts, turn);
+    if (LANES)
+      st = warp_join<LANES ? LANES : 32>(st, codes);
+    else
+      st = block_join(st, codes, parts, turn);
     write_row<VPT>(a, m, lane, width, vecs, st, h);
   }
 }
@@ -248,8 +251,8 @@ __global__ void __launch_bounds__(any_threads(E), any_blocks(VEC, E)) norm_any_k
         }
       }
     }
-    st = block_join(warp_join(st), parts, turn);
-    const float factor = row_factor(st.ss, a.K, a.eps);
+    st = block_join(st, codes, parts, turn);
+    const float factor = row_factor(st.ss, a);
     const Divisor scale(codes ? row_scale(st.peak, factor) : 1.0f);
     if (codes && tid == 0) a.out_scales[m] = scale.scale;
     for (int base = 0; base < pieces; base += span) {
@@ -272,26 +275,35 @@ __global__ void __launch_bounds__(any_threads(E), any_blocks(VEC, E)) norm_any_k
 
 namespace {
 
-template <int TX, int TR, int VPT, bool WARP>
+template <int TX, int TR, int VPT, int LANES>
 cudaError_t launch_norm(const NormArgs& a, int threads, int num_sms, cudaStream_t s, int* launches) {
-  const int64_t per = WARP ? threads / 32 : 1;
-  const int resident = std::min(32, norm_threads(WARP) * norm_blocks(VPT, WARP) / threads);  // blocks an SM
+  const int64_t per = LANES ? threads / LANES : 1;
+  const int resident = std::min(32, norm_threads(LANES) * norm_blocks(VPT, LANES) / threads);  // blocks an SM
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ceil_div(a.M, per), static_cast<int64_t>(resident) * num_sms));
-  return launch_early(norm_kernel<TX, TR, VPT, WARP>, dim3(blocks), threads, 0, s, launches, a);
+  return launch_early(norm_kernel<TX, TR, VPT, LANES>, dim3(blocks), threads, 0, s, launches, a);
 }
 
 template <int TX, int TR>
 cudaError_t launch_norm_types(const NormArgs& a, int num_sms, cudaStream_t s, int* launches) {
   const int64_t vecs = a.K / 8;
-  if (vecs <= 128 && a.M > num_sms) {  // a warp per row
-    if (vecs <= 32) return launch_norm<TX, TR, 1, true>(a, 256, num_sms, s, launches);
-    return launch_norm<TX, TR, 4, true>(a, 256, num_sms, s, launches);
+  if (vecs <= 128 && a.M > num_sms) {  // rows of a warp or of a part of one
+    if (vecs <= 8) return launch_norm<TX, TR, 1, 8>(a, 256, num_sms, s, launches);
+    if (vecs <= 16) return launch_norm<TX, TR, 1, 16>(a, 256, num_sms, s, launches);
+    if (vecs <= 32) return launch_norm<TX, TR, 1, 32>(a, 256, num_sms, s, launches);
+    return launch_norm<TX, TR, 4, 32>(a, 256, num_sms, s, launches);
   }
-  const int vpt = vecs <= 512 ? 1 : (vecs <= 1024 ? 2 : 4);
+  // More vectors a thread share a warp's fixed cost of a row, fewer leave more warps to a row. With
+  // rows enough for both: without a residual, 16384 rows of 4096 in bf16 take 46 us at two and 56 at one;
+  // with one, 16384 rows of 8192 take 168 us at four and 173 at two, but as e4m3, whose output
+  // has more instructions, 8192 rows of 7168 take 71 and 66.
+  const bool many = a.M > 8 * num_sms;
+  const int vpt = vecs <= 512    ? (many && TR == kTypeNone ? 2 : 1)
+                  : vecs <= 1024 ? (many && TR != kTypeNone && a.out_type != kTypeE4m3 ? 4 : 2)
+                                 : 4;
   const int threads = static_cast<int>(ceil_div(ceil_div(vecs, vpt), 32) * 32);
-  if (vpt == 1) return launch_norm<TX, TR, 1, false>(a, threads, num_sms, s, launches);
-  if (vpt == 2) return launch_norm<TX, TR, 2, false>(a, threads, num_sms, s, launches);
-  return launch_norm<TX, TR, 4, false>(a, threads, num_sms, s, launches);
+  if (vpt == 1) return launch_norm<TX, TR, 1, 0>(a, threads, num_sms, s, launches);
+  if (vpt == 2) return launch_norm<TX, TR, 2, 0>(a, threads, num_sms, s, launches);
+  return launch_norm<TX, TR, 4, 0>(a, threads, num_sms, s, launches);
 }
 
 template <int TX>

@@ -107,6 +107,17 @@ def test_norm_sizes(M, K):
     _check_norm(X, w, awq.rms_norm(X, w, out_dtype=E4M3))
 
 
+@pytest.mark.parametrize("out", [F16, E4M3])
+@pytest.mark.parametrize("x,r", [(BF16, None), (F16, BF16), (F32, None), (F32, F32)])
+@pytest.mark.parametrize("K", [8, 64, 65, 120, 250, 500, 1001, 1032, 2047, 4096, 4104, 5000, 8190])
+def test_norm_many_rows(x, r, out, K):
+    """More rows than a grid holds several times over."""
+    M = 1500 if K > 1000 else 5003
+    X, w, R = _randn(M, K, dtype=x, seed=K), _randn(K, seed=2), None if r is None else _randn(M, K, dtype=r, seed=3)
+    new = None if r is None else torch.empty_like(R)
+    _check_norm(X, w, awq.rms_norm(X, w, residual=R, residual_out=new, out_dtype=out), R, new)
+
+
 @pytest.mark.parametrize("K,pitch,offset", [(256, 264, 0), (256, 257, 0), (256, 264, 1), (4096, 4104, 8), (100, 128, 4), (2048, 2050, 2), (12288, 12296, 0)])
 def test_norm_strides_and_offsets(K, pitch, offset):
     M = 9
