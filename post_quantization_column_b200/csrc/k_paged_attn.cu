@@ -35,10 +35,10 @@
 // token per sequence the tensor pipe is 4 % busy here.
 //
 // Measured (B200, device time in a captured graph; the copy rate is 6.55 TB/s): 16 x 4096 tokens
-// of 32 fp16 heads 162 us, 6.6 TB/s; 67 ragged sequences up to 8192, 8 bf16 heads shared by 64,
+// of 32 fp16 heads 163 us, 6.6 TB/s; 67 ragged sequences up to 8192, 8 bf16 heads shared by 64,
 // 189 us, 6.4 TB/s; one sequence of 131072 tokens 88 us, 6.1 TB/s; 96 ragged sequences up to
-// 4099 on an e4m3 cache 95 us, 4.6 TB/s (bound by the latency of a tile's chain: 131 of its 560
-// instructions unpack e4m3; 6.7 TB/s at the margin of longer sequences); one of 33 tokens 4.8 us.
+// 4099 on an e4m3 cache 96 us, 4.6 TB/s (bound by the latency of a tile's chain: 131 of its 560
+// instructions unpack e4m3; 6.7 TB/s at the margin of longer sequences); one of 33 tokens 4.9 us.
 #include "decode_kernels.h"
 
 #include <algorithm>
