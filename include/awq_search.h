@@ -376,7 +376,7 @@ int awq_w4a16_dequant(const int32_t* codes, const void* steps, const void* zeros
  *   y[m][k] = h[m][k] weight[k] / sqrt(mean_k h[m][k]^2 + eps)   (statistics in fp32, of the
  *   unrounded h; rounded once to out_dtype)
  * X [M][K], residual and residual_out [M][K] (may be NULL together; residual_out may be
- * `residual` itself; otherwise it, and `out`, overlap no other argument) and weight [K] each hold
+ * `residual` itself; otherwise it, and `out`, meet no row of another argument) and weight [K] each hold
  * AWQ_DTYPE_F32, _F16 or _BF16; rows x_stride, r_stride and ro_stride apart. out [M][K]
  * contiguous holds one of these types, or AWQ_DTYPE_E4M3: out_scales[m] = max_k |y| / 448 (1
  * where that is zero) and out = e4m3(y / out_scales[m]); a row with a NaN or an infinity has

@@ -20,10 +20,14 @@ constexpr int64_t kIntMax = (int64_t(1) << 31) - 1;
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool is_float(int t) { return t == kTypeF32 || t == kTypeF16 || t == kTypeBf16; }
 
-// Whether [a, a + rows) and [b, b + rows) of `bytes` each, `sa` and `sb` bytes apart, meet.
+// Whether the rows of a and of b, `wa` and `wb` bytes each and `sa` and `sb` bytes apart, meet; rows at
+// one distance may lie between each other (columns of one buffer).
 bool ranges_meet(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb, int64_t wb, int64_t rows) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + (rows - 1) * sb + wb && b0 < a0 + (rows - 1) * sa + wa;
+  if (a0 >= b0 + (rows - 1) * sb + wb || b0 >= a0 + (rows - 1) * sa + wa) return false;
+  if (sa != sb || sa < wa + wb) return true;
+  const int64_t apart = static_cast<int64_t>(b0 - a0) % sa, d = apart < 0 ? apart + sa : apart;  // from a row of a to the next of b
+  return d < wa || d + wb > sa;
 }
 
 constexpr int kAsk = -1;  // the device of the call is asked of its pointers
@@ -112,8 +116,8 @@ int awq_rms_norm_on(int device, const void* X, int x_dtype, int64_t x_stride, co
   if ((residual == nullptr) != (residual_out == nullptr))
     return decode_error(AWQ_ERR_INVALID_ARG, "residual and residual_out come together");
   if (out_dtype == kTypeE4m3 && !out_scales) return decode_error(AWQ_ERR_INVALID_ARG, "an e4m3 output needs out_scales");
-  const int xb = type_bytes(x_dtype), rb = residual ? type_bytes(r_dtype) : 1, ob = type_bytes(out_dtype);
-  if (!aligned(X, xb) || !aligned(weight, type_bytes(w_dtype)) || !aligned(out, ob) || !aligned(out_scales, 4) ||
+  const int xb = type_bytes(x_dtype), wb = type_bytes(w_dtype), rb = residual ? type_bytes(r_dtype) : 1, ob = type_bytes(out_dtype);
+  if (!aligned(X, xb) || !aligned(weight, wb) || !aligned(out, ob) || !aligned(out_scales, 4) ||
       !aligned(residual, rb) || !aligned(residual_out, rb))
     return decode_error(AWQ_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
   if (x_stride < 0 || (residual && (r_stride < 0 || ro_stride < K)))
@@ -121,10 +125,11 @@ int awq_rms_norm_on(int device, const void* X, int x_dtype, int64_t x_stride, co
   if (residual) {
     const bool same = residual == residual_out && r_stride == ro_stride;
     if ((!same && ranges_meet(residual, r_stride * rb, K * rb, residual_out, ro_stride * rb, K * rb, M)) ||
-        ranges_meet(X, x_stride * xb, K * xb, residual_out, ro_stride * rb, K * rb, M))
+        ranges_meet(X, x_stride * xb, K * xb, residual_out, ro_stride * rb, K * rb, M) ||
+        ranges_meet(weight, 0, K * wb, residual_out, ro_stride * rb, K * rb, M))
       return decode_error(AWQ_ERR_INVALID_ARG, "residual_out may be the residual itself but overlap nothing else");
   }
-  if (ranges_meet(X, x_stride * xb, K * xb, out, K * ob, K * ob, M) ||
+  if (ranges_meet(X, x_stride * xb, K * xb, out, K * ob, K * ob, M) || ranges_meet(weight, 0, K * wb, out, K * ob, K * ob, M) ||
       (residual && (ranges_meet(residual, r_stride * rb, K * rb, out, K * ob, K * ob, M) ||
                     ranges_meet(residual_out, ro_stride * rb, K * rb, out, K * ob, K * ob, M))))
     return decode_error(AWQ_ERR_INVALID_ARG, "out must not overlap another argument");

@@ -326,10 +326,11 @@ bool rows_aligned(const NormArgs& a, int vec) {
          (!a.residual || (whole(a.residual, a.r_stride, a.r_type) && whole(a.residual_out, a.ro_stride, a.r_type)));
 }
 
-// Whether row m of every tensor starts (m K) mod 8 values beyond a whole vector.
+// Whether row m of every tensor starts (m K) mod 8 values beyond a whole vector, and the next row
+// behind its end (whose values a row's last window may read).
 bool rows_shifted(const NormArgs& a) {
   auto like = [&](const void* p, int64_t stride, int type) {
-    return reinterpret_cast<uintptr_t>(p) % std::min(16, 8 * type_bytes(type)) == 0 && (a.M == 1 || (stride - a.K) % 8 == 0);
+    return reinterpret_cast<uintptr_t>(p) % std::min(16, 8 * type_bytes(type)) == 0 && (a.M == 1 || (stride >= a.K && (stride - a.K) % 8 == 0));
   };
   return like(a.X, a.x_stride, a.x_type) && like(a.out, a.K, a.out_type) &&
          (!a.residual || (like(a.residual, a.r_stride, a.r_type) && like(a.residual_out, a.ro_stride, a.r_type)));

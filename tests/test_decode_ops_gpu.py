@@ -134,6 +134,30 @@ def test_norm_strides_and_offsets(K, pitch, offset):
     _check_norm(Xe, w, awq.rms_norm(Xe, w))
 
 
+@pytest.mark.parametrize("K", [96, 515])
+def test_norm_columns_of_one_buffer(K):
+    """X and a residual that is replaced in place, side by side in one buffer; rows that overlap."""
+    M, w = 40, _randn(K, seed=6)
+    for pitch, at in ((2 * K, K), (3 * K + 5, K), (2 * K + 64, K + 64)):
+        buf = _randn(M, pitch, seed=5)
+        before = buf.clone()
+        X, R = buf[:, :K], buf[:, at:at + K]
+        _check_norm(before[:, :K], w, awq.rms_norm(X, w, residual=R), before[:, at:at + K], R)
+        kept = torch.ones(pitch, dtype=torch.bool, device="cuda")
+        kept[at:at + K] = False
+        assert torch.equal(buf[:, kept], before[:, kept])
+        with pytest.raises(awq.AwqError):
+            awq.rms_norm(X, w, residual=buf[:, K - 1:2 * K - 1])
+        with pytest.raises(awq.AwqError):
+            awq.rms_norm(buf[:, 1:1 + K], w, residual=buf[:, :K])
+    flat = _randn(M + K, seed=7)
+    for step in (1, K % 8 or 8):
+        Xh = torch.as_strided(flat, (1 + M // step, K), (step, 1))
+        _check_norm(Xh, w, awq.rms_norm(Xh, w))
+    with pytest.raises(awq.AwqError):
+        awq.rms_norm(_randn(M, K, seed=8), buf[3, :K], residual=buf[:, :K])
+
+
 @pytest.mark.parametrize("K", [512, 515])
 def test_norm_special_rows(K):
     X, w = _randn(6, K, seed=9), _randn(K, seed=10)
