@@ -32,7 +32,7 @@
 // cp.async stages took twice the time: eight warps' chains of shared-memory reads, shuffles
 // and products were longer than the loads; bulk copies of 128-byte rows stop at 3.9 TB/s.)
 // The MMAs are mma.sync: tcgen05 wants 64 rows or more of a tile in shared memory, and at one
-// token per sequence the tensor pipe is 4 % busy here.
+// token per sequence the tensor pipe is 10 % busy here.
 //
 // Measured (B200, device time in a captured graph; the copy rate is 6.55 TB/s): 16 x 4096 tokens
 // of 32 fp16 heads 163 us, 6.6 TB/s; 67 ragged sequences up to 8192, 8 bf16 heads shared by 64,
