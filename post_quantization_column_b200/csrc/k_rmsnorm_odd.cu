@@ -54,25 +54,25 @@ __device__ __forceinline__ void store_window(void* row, int first, int K, const 
 }
 
 // Blocks of up to 544 threads: 8192 values and a row's ends in two windows each.
-constexpr int threads_of(bool warp) { return warp ? 256 : 544; }
+constexpr int threads_of(int lanes) { return lanes ? 256 : 544; }
 // of that size an SM
-constexpr int blocks_of(int vpt, bool warp, bool wide) {
-  return warp ? (vpt == 1 ? 5 - wide : (vpt == 2 ? 4 - wide : 2)) : (vpt + wide <= 2 ? 2 : 1);
+constexpr int blocks_of(int vpt, int lanes, bool wide) {
+  return lanes ? (vpt == 1 ? 5 - wide : (vpt == 2 ? 4 - wide : 2)) : (vpt + wide <= 2 ? 2 : 1);
 }
-template <int TX, int TR, int VPT, bool WARP>
-__global__ void __launch_bounds__(threads_of(WARP), blocks_of(VPT, WARP, TX == kTypeF32 || TR == kTypeF32)) norm_shifted_kernel(NormArgs a) {
+template <int TX, int TR, int VPT, int LANES>
+__global__ void __launch_bounds__(threads_of(LANES), blocks_of(VPT, LANES, TX == kTypeF32 || TR == kTypeF32)) norm_shifted_kernel(NormArgs a) {
   extern __shared__ float weight[];
   __shared__ RowStat parts[2][32];
   int turn = 0;
-  const int tid = WARP ? threadIdx.x % 32 : threadIdx.x, width = WARP ? 32 : blockDim.x, K = static_cast<int>(a.K);
-  const int rows = WARP ? blockDim.x / 32 : 1;
+  const int tid = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x, width = LANES ? LANES : blockDim.x, K = static_cast<int>(a.K);
+  const int rows = LANES ? blockDim.x / width : 1;
   const bool codes = a.out_type == kTypeE4m3;
   wait_for_previous();
   start_next();
   for (int e = static_cast<int>(threadIdx.x) - 8; e < K + 8; e += blockDim.x)
     weight[weight_place(e)] = e >= 0 && e < K ? load_one(a.weight, e, a.w_type) : 0.0f;
   __syncthreads();
-  for (int64_t m = static_cast<int64_t>(blockIdx.x) * rows + (WARP ? threadIdx.x / 32 : 0); m < a.M;
+  for (int64_t m = static_cast<int64_t>(blockIdx.x) * rows + (LANES ? threadIdx.x / width : 0); m < a.M;
        m += static_cast<int64_t>(gridDim.x) * rows) {
     const int shift = static_cast<int>(m * a.K % 8), vecs = (K + shift + 7) / 8;
     const void* x = row_at(a.X, m * a.x_stride, TX);
@@ -123,7 +123,10 @@ __global__ void __launch_bounds__(threads_of(WARP), blocks_of(VPT, WARP, TX == k
         for (int k = 0; k < 8; ++k) st.peak = max(st.peak, __float_as_uint(h[i][k]) & 0x7FFFFFFFu);
       }
     }
-    st = WARP ? warp_join(st, codes) : block_join(st, codes, parts, turn);
+    if (LANES)
+      st = warp_join<LANES ? LANES : 32>(st, codes);
+    else
+      st = block_join(st, codes, parts, turn);
     const float factor = row_factor(st.ss, a);
     const Divisor scale(codes ? row_scale(st.peak, factor) : 1.0f);
     if (codes && tid == 0) a.out_scales[m] = scale.scale;
@@ -147,33 +150,34 @@ __global__ void __launch_bounds__(threads_of(WARP), blocks_of(VPT, WARP, TX == k
   }
 }
 
-template <int TX, int TR, int VPT, bool WARP>
+template <int TX, int TR, int VPT, int LANES>
 cudaError_t launch(const NormArgs& a, int num_sms, cudaStream_t s, int* launches) {
-  const int threads = WARP ? 256 : static_cast<int>(ceil_div(ceil_div(a.K / 8 + 2, VPT), 32) * 32);
+  const int threads = LANES ? 256 : static_cast<int>(ceil_div(ceil_div(a.K / 8 + 2, VPT), 32) * 32);
   const size_t smem = static_cast<size_t>(a.K + 16 + (a.K + 16) / 8 + 1) * 4;
   static unsigned long long done = 0;
-  const cudaError_t e = set_smem_limit_once(norm_shifted_kernel<TX, TR, VPT, WARP>, 80 * 1024, &done);
+  const cudaError_t e = set_smem_limit_once(norm_shifted_kernel<TX, TR, VPT, LANES>, 80 * 1024, &done);
   if (e != cudaSuccess) return e;
-  const int64_t resident = std::min<int64_t>(std::min(32, threads_of(WARP) * blocks_of(VPT, WARP, TX == kTypeF32 || TR == kTypeF32) / threads), 220 * 1024 / (smem + 2048));
-  const int64_t rows = WARP ? threads / 32 : 1;
+  const int64_t resident = std::min<int64_t>(std::min(32, threads_of(LANES) * blocks_of(VPT, LANES, TX == kTypeF32 || TR == kTypeF32) / threads), 220 * 1024 / (smem + 2048));
+  const int64_t rows = LANES ? threads / (LANES ? LANES : 1) : 1;
   const unsigned blocks = static_cast<unsigned>(std::min(ceil_div(a.M, rows), resident * num_sms));
-  return launch_early(norm_shifted_kernel<TX, TR, VPT, WARP>, dim3(blocks), threads, smem, s, launches, a);
+  return launch_early(norm_shifted_kernel<TX, TR, VPT, LANES>, dim3(blocks), threads, smem, s, launches, a);
 }
 
 template <int TX, int TR>
 cudaError_t launch_types(const NormArgs& a, int num_sms, cudaStream_t s, int* launches) {
   const int64_t vecs = a.K / 8 + 2;
-  if (vecs <= 128 && a.M > num_sms) {  // a warp per row
-    if (vecs <= 32) return launch<TX, TR, 1, true>(a, num_sms, s, launches);
-    if (vecs <= 64) return launch<TX, TR, 2, true>(a, num_sms, s, launches);
-    return launch<TX, TR, 4, true>(a, num_sms, s, launches);
+  if (vecs <= 128 && a.M > num_sms) {  // rows of a warp or of half of one
+    if (vecs <= 16) return launch<TX, TR, 1, 16>(a, num_sms, s, launches);
+    if (vecs <= 32) return launch<TX, TR, 1, 32>(a, num_sms, s, launches);
+    if (vecs <= 64) return launch<TX, TR, 2, 32>(a, num_sms, s, launches);
+    return launch<TX, TR, 4, 32>(a, num_sms, s, launches);
   }
   // With rows enough, two windows a thread share a warp's fixed cost of a row: 16384 rows of 3333 in
   // fp16 take 81 us so, 97 with one; in fp32, where two leave one block an SM, 10000 of 4099 take 122 and 70.
   const bool many = a.M > 8 * num_sms && TX != kTypeF32 && TR != kTypeF32;
-  if (vecs <= threads_of(false) && !many) return launch<TX, TR, 1, false>(a, num_sms, s, launches);
-  if (vecs <= 2 * threads_of(false)) return launch<TX, TR, 2, false>(a, num_sms, s, launches);
-  return launch<TX, TR, 4, false>(a, num_sms, s, launches);
+  if (vecs <= threads_of(0) && !many) return launch<TX, TR, 1, 0>(a, num_sms, s, launches);
+  if (vecs <= 2 * threads_of(0)) return launch<TX, TR, 2, 0>(a, num_sms, s, launches);
+  return launch<TX, TR, 4, 0>(a, num_sms, s, launches);
 }
 
 template <int TX>
