@@ -33,14 +33,17 @@ bool ranges_meet(const void* a, int64_t sa, int64_t wa, const void* b, int64_t s
 constexpr int kAsk = -1;  // the device of the call is asked of its pointers
 
 // Makes the device of the call current: the caller's, which owns all its pointers (the Python
-// binding knows its tensors' device), or that of `first`, where every pointer must lie.
-int take_device(int device, const void* first, const void* const* ptrs, int n, int* num_sms) {
+// binding knows its tensors' device), or that of `first`, where every pointer must lie. A kernel that
+// meets a bad page stores to `status` (may be NULL), so an address that it cannot reach is refused here.
+int take_device(int device, const void* first, const void* const* ptrs, int n, const int32_t* status, int* num_sms) {
   int dev = device;
   const int st = decode_device(first, &dev, num_sms);
   if (st != AWQ_OK || device != kAsk) return st;
   for (int i = 0; i < n; ++i)
     if (ptrs[i] && !decode_device_memory(ptrs[i], dev))
       return decode_error(AWQ_ERR_INVALID_ARG, "inputs and outputs must be memory of the device the call runs on");
+  if (status && !decode_status_memory(status, dev))
+    return decode_error(AWQ_ERR_INVALID_ARG, "status must be memory of the device the call runs on, or pinned host memory");
   return AWQ_OK;
 }
 
@@ -137,7 +140,7 @@ int awq_rms_norm_on(int device, const void* X, int x_dtype, int64_t x_stride, co
   DeviceRestore restore_device;
   const void* ptrs[] = {X, residual, residual_out, weight, out, out_dtype == kTypeE4m3 ? out_scales : nullptr};
   int num_sms = 0;
-  const int st = take_device(device, X, ptrs, 6, &num_sms);
+  const int st = take_device(device, X, ptrs, 6, nullptr, &num_sms);
   if (st != AWQ_OK) return st;
   NormArgs a;
   a.X = X;
@@ -245,7 +248,7 @@ int awq_kv_append_on(int device, const void* q, int64_t q_token_stride, int64_t 
   const void* ptrs[] = {k, v, positions, a.c.k, a.c.v, a.c.table, Hq > 0 ? q : nullptr, Hq > 0 ? q_out : nullptr, seqs,
                         rotary_dim > 0 ? freqs : nullptr, a.c.k_scale, a.c.v_scale};
   int num_sms = 0;
-  if ((st = take_device(device, k, ptrs, 12, &num_sms)) != AWQ_OK) return st;
+  if ((st = take_device(device, k, ptrs, 12, status, &num_sms)) != AWQ_OK) return st;
   a.q = q;
   a.k = k;
   a.v = v;
@@ -314,7 +317,7 @@ int awq_paged_attention_on(int device, const void* q, int64_t q_seq_stride, int6
   DeviceRestore restore_device;
   const void* ptrs[] = {q, a.c.k, a.c.v, a.c.table, lengths, out, workspace, a.c.k_scale, a.c.v_scale};
   int num_sms = 0;
-  if ((st = take_device(device, q, ptrs, 9, &num_sms)) != AWQ_OK) return st;
+  if ((st = take_device(device, q, ptrs, 9, status, &num_sms)) != AWQ_OK) return st;
   a.q = q;
   a.q_sb = q_seq_stride;
   a.q_sh = q_head_stride;

@@ -91,6 +91,7 @@ int decode_cuda_error(cudaError_t e, const char* where);
 // Makes device *dev current, or for -1 the device that owns `ptr`, and checks it once.
 int decode_device(const void* ptr, int* dev, int* num_sms);
 bool decode_device_memory(const void* p, int dev);  // memory of device `dev`, or managed memory
+bool decode_status_memory(const void* p, int dev);  // the same, or pinned host memory that kernels reach at `p`
 void record_launch_count(int launches);
 
 #ifdef __CUDACC__

@@ -1,0 +1,73 @@
+"""Calls of the decode-step operators that their other tests do not make (B200 only): the C ABI
+with addresses that it has to refuse, and the binding under autograd, threads and streams."""
+import ctypes
+import struct
+
+import pytest
+import torch
+
+import post_quantization_column_b200 as awq
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16, E4M3 = torch.float32, torch.float16, torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def _randn(*shape, dtype=F32, seed=0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+
+
+class _Step:
+    """One append and one attention of two sequences, four query heads on two, through the C ABI."""
+
+    def __init__(self, page=16, pages=4, **cache):
+        self.k, self.v = (_randn(2, 2, 128, dtype=F16, seed=i) for i in (1, 2))
+        self.q = _randn(2, 4, 128, dtype=F16, seed=3)
+        self.caches = [_randn(pages, page, 2, 128, dtype=F16, seed=i) for i in (4, 5)]
+        self.table = torch.tensor([[1], [3]], dtype=torch.int32, device="cuda")
+        self.pos = torch.tensor([4, 9], dtype=torch.int32, device="cuda")
+        self.lens = self.pos + 1
+        self.out = torch.full((2, 4, 128), 7.0, dtype=F16, device="cuda")
+        self.freqs = awq.rope_frequencies(128)[0]
+        size = awq.library().awq_paged_attention_workspace(4, 2, 128, 2)
+        self.ws, self.ws_bytes = torch.empty(size, dtype=torch.uint8, device="cuda"), size
+        d = dict(k=self.caches[0].data_ptr(), v=self.caches[1].data_ptr(), dtype=2, num_pages=pages, page_size=page, heads=2, head_dim=128,
+                 ps=page * 256, ss=256, hs=128, ks=0, vs=0, table=self.table.data_ptr(), seqs=2, max_pages=1, ts=1)
+        self.desc = struct.pack("@16q", *{**d, **cache}.values())
+        torch.cuda.synchronize()
+
+    def append(self, status=None, **kw):
+        a = dict(q=self.q.data_ptr(), qs=512, qh=128, k=self.k.data_ptr(), ks=256, kh=128, v=self.v.data_ptr(), vs=256, vh=128, it=2,
+                 T=2, Hq=4, qo=self.out.data_ptr(), qt=2, pos=self.pos.data_ptr(), seq=None, f=self.freqs.data_ptr(), rot=128, il=0, mag=1.0,
+                 c=self.desc, st=status, s=ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        a.update(kw)
+        return awq.library().awq_kv_append(*a.values())
+
+    def attend(self, status=None, **kw):
+        a = dict(q=self.q.data_ptr(), qs=512, qh=128, qt=2, Hq=4, c=self.desc, len=self.lens.data_ptr(), scale=0.1, out=self.out.data_ptr(),
+                 ws=self.ws.data_ptr(), wb=self.ws_bytes, st=status, s=ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        a.update(kw)
+        return awq.library().awq_paged_attention(*a.values())
+
+
+def test_status_of_memory_that_a_kernel_cannot_reach_is_refused():
+    """A plain host int as the status word: the store that reports a bad page would go astray, so the
+    call is refused before any launch (every page here is good, and nothing is written)."""
+    step = _Step()
+    before = [c.clone() for c in step.caches]
+    word = (ctypes.c_int32 * 4)()
+    for call in (step.append, step.attend):
+        assert call(ctypes.c_void_p(ctypes.addressof(word))) == 1
+        assert b"status" in awq.library().awq_last_error_message()
+    torch.cuda.synchronize()
+    assert (step.out == 7.0).all() and all(torch.equal(a, b) for a, b in zip(before, step.caches)) and not any(word)
+    for status in (torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32).pin_memory()):
+        assert step.append(status.data_ptr()) == 0 and step.attend(status.data_ptr()) == 0
+        torch.cuda.synchronize()
+        assert int(status) == 0
