@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import post_quantization_column_b200 as awq
+from tests.test_decode_ops_gpu import _check_norm
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +72,69 @@ def test_status_of_memory_that_a_kernel_cannot_reach_is_refused():
         assert step.append(status.data_ptr()) == 0 and step.attend(status.data_ptr()) == 0
         torch.cuda.synchronize()
         assert int(status) == 0
+
+
+# ---- forms of the RMS norm that take rows too long for registers, value by value or in pairs ----------
+
+@pytest.mark.parametrize("K", [16385, 20001, 57343, 16386, 30002, 57342])
+@pytest.mark.parametrize("M", [3, 170])
+def test_long_rows_of_odd_and_even_length(M, K):
+    X, w, R = _randn(M, K, dtype=BF16, seed=K), _randn(K, dtype=BF16, seed=2), _randn(M, K, seed=3)
+    new = torch.empty_like(R)
+    _check_norm(X, w, awq.rms_norm(X, w, residual=R, residual_out=new), R, new)
+    _check_norm(X, w, awq.rms_norm(X, w, out_dtype=E4M3))
+
+
+@pytest.mark.parametrize("offset", [1, 2])
+def test_long_rows_that_start_between_vectors(offset):
+    M, K = 5, 28672
+    base, rbase, w = _randn(M, K + 2, dtype=F16, seed=4), _randn(M, K + 2, dtype=BF16, seed=5), _randn(K, seed=6)
+    X, R = base[:, offset:offset + K], rbase[:, offset:offset + K]
+    before = rbase.clone()
+    for out in (F16, E4M3):
+        R.copy_(before[:, offset:offset + K])
+        _check_norm(X, w, awq.rms_norm(X, w, residual=R, out_dtype=out), before[:, offset:offset + K], R)
+    rbase[:, offset:offset + K] = before[:, offset:offset + K]
+    assert torch.equal(rbase, before)   # nothing beside the rows was written
+
+
+# ---- the binding -----------------------------------------------------------------------------------
+
+
+_CAPTURED_FIRST = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import post_quantization_column_b200 as awq
+g = torch.Generator().manual_seed(0)
+X, w = torch.randn(3, 20002, generator=g).cuda(), torch.randn(20002, generator=g).cuda()
+rows = torch.randn(2, 8, 128, generator=g).half().cuda()
+caches = [torch.randn(4, 16, 2, 128, generator=g).half().cuda() for _ in range(2)]
+kept = [c.clone() for c in caches]
+table, pos = torch.tensor([[1], [3]], dtype=torch.int32).cuda(), torch.tensor([4, 9], dtype=torch.int32).cuda()
+lens, freqs = pos + 1, awq.rope_frequencies(128)[0]
+
+def step(kc, vc):
+    q = awq.kv_append(rows[:, :4], rows[:, 4:6], rows[:, 6:], kc, vc, table, pos, freqs)
+    return awq.rms_norm(X, w), q, awq.paged_attention(q, kc, vc, table, lens)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step(*caches)
+graph.replay()
+torch.cuda.synchronize()
+want = step(*kept)
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and all(torch.equal(a, b) for a, b in zip(caches, kept))
+print("captured first: ok")
+"""
+
+
+def test_a_first_call_may_be_a_captured_one():
+    """In a new process, with nothing of the library used before the capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", _CAPTURED_FIRST.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "captured first: ok" in done.stdout, done.stdout + done.stderr
