@@ -77,6 +77,11 @@ void on_device(const Tensor& t, const at::Device& device) {
               "the decode-step operators have no backward pass: call them under torch.no_grad()");
 }
 
+// Tells autograd that `t` has been written, so that a backward pass that saved it is an error.
+void written(const Tensor& t) {
+  if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 Tensor empty(at::IntArrayRef sizes, at::ScalarType t, const at::Device& device) {
   return at::detail::empty_cuda(sizes, t, device, std::nullopt);
 }
@@ -202,6 +207,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                    rc, r_stride, into.defined() ? into.data_ptr() : nullptr, ro_stride, weight.data_ptr(), wc, M,
                                    K, static_cast<float>(eps), out.data_ptr(), oc,
                                    scales.defined() ? scales.data_ptr<float>() : nullptr, current_stream(device));
+    if (st == AWQ_OK) written(into);
     if (st != AWQ_OK || !scales.defined()) return result(st, out);
     return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(scales));
   });
@@ -255,6 +261,8 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
         rot ? freqs.data_ptr<double>() : nullptr, static_cast<int>(rot), interleaved, static_cast<float>(magnitude), &cache,
         status_word(status, device), current_stream(device));
     if (st != AWQ_OK) return PyLong_FromLong(st);
+    written(k_cache);
+    written(v_cache);
     if (!out.defined()) Py_RETURN_NONE;
     return THPVariable_Wrap(out);
   });

@@ -100,6 +100,38 @@ def test_long_rows_that_start_between_vectors(offset):
 
 # ---- the binding -----------------------------------------------------------------------------------
 
+def _decode_inputs():
+    k, v, q = _randn(2, 2, 128, dtype=F16, seed=1), _randn(2, 2, 128, dtype=F16, seed=2), _randn(2, 4, 128, dtype=F16, seed=3)
+    kc, vc = (_randn(4, 16, 2, 128, dtype=F16, seed=i) for i in (4, 5))
+    table = torch.tensor([[1], [3]], dtype=torch.int32, device="cuda")
+    return q, k, v, kc, vc, table, torch.tensor([4, 9], dtype=torch.int32, device="cuda")
+
+
+def test_tensors_that_autograd_saved_are_written_openly():
+    """An in-place write of a tensor that a backward pass still needs makes that pass an error."""
+    q, k, v, kc, vc, table, pos = _decode_inputs()
+    X, w, r = _randn(4, 64, seed=6), _randn(64, seed=7), _randn(4, 64, seed=8)
+    for write, saved in ((lambda: awq.rms_norm(X, w, residual=r), [r]),
+                         (lambda: awq.rms_norm(X, w, residual=X * 2, residual_out=r), [r]),
+                         (lambda: awq.kv_append(q, k, v, kc, vc, table, pos), [kc, vc]),
+                         (lambda: awq.kv_append(q, k, v, kc[:], vc[:], table, pos), [kc, vc])):
+        for t in saved:
+            leaf = torch.ones_like(t, requires_grad=True)
+            loss = (t * leaf).sum()
+            write()
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+    versions = [t._version for t in (X, w, q, k, v, table, pos)]
+    awq.kv_append(q, k, v, kc, vc, table, pos)
+    awq.rms_norm(X, w)
+    awq.paged_attention(q, kc, vc, table, pos + 1)
+    assert versions == [t._version for t in (X, w, q, k, v, table, pos)]   # inputs that are only read
+    with torch.inference_mode():                       # tensors without a version
+        ri, kci, vci = r.clone(), kc.clone(), vc.clone()
+        awq.rms_norm(X, w, residual=ri)
+        awq.kv_append(q, k, v, kci, vci, table, pos)
+    assert torch.equal(kci, kc) and torch.equal(vci, vc)
+
 
 _CAPTURED_FIRST = """
 import sys
