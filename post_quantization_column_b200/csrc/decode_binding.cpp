@@ -7,6 +7,7 @@
 // stream and returns the output tensors, or the library's status as an int when that is not OK.
 #include <ATen/cuda/CUDAContext.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/grad_mode.h>
@@ -69,12 +70,14 @@ const Tensor& tensor(PyObject* o, const char* what) {
 // An optional tensor: undefined for None.
 Tensor maybe(PyObject* o, const char* what) { return o == Py_None ? Tensor() : tensor(o, what); }
 
-// The tensor lies on `device` and carries no gradient.
+// The tensor lies on `device` and carries no gradient, of backward or of forward mode.
 void on_device(const Tensor& t, const at::Device& device) {
   if (!t.defined()) return;
   value_check(t.device() == device, "every tensor must be on the device of the first");
   value_check(!(t.requires_grad() && at::GradMode::is_enabled()),
               "the decode-step operators have no backward pass: call them under torch.no_grad()");
+  value_check(!(c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined()),
+              "the decode-step operators have no forward-mode derivative: pass tensors without tangents");
 }
 
 // Tells autograd that `t` has been written, so that a backward pass that saved it is an error.

@@ -133,6 +133,20 @@ def test_tensors_that_autograd_saved_are_written_openly():
     assert torch.equal(kci, kc) and torch.equal(vci, vc)
 
 
+def test_forward_mode_tangents_are_refused():
+    import torch.autograd.forward_ad as fwd
+    q, k, v, kc, vc, table, pos = _decode_inputs()
+    X, w, r = _randn(4, 64, seed=6), _randn(64, seed=7), _randn(4, 64, seed=8)
+    with fwd.dual_level():
+        dual = lambda t: fwd.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for bad in (lambda: awq.rms_norm(dual(X), w), lambda: awq.rms_norm(X, dual(w)), lambda: awq.rms_norm(X, w, residual=dual(r)),
+                    lambda: awq.kv_append(dual(q), k, v, kc, vc, table, pos), lambda: awq.kv_append(q, k, dual(v), kc, vc, table, pos),
+                    lambda: awq.paged_attention(dual(q), kc, vc, table, pos + 1), lambda: awq.paged_attention(q, dual(kc), vc, table, pos + 1)):
+            with torch.no_grad(), pytest.raises(ValueError):   # no_grad leaves forward mode on
+                bad()
+        awq.rms_norm(X, w)
+
+
 _CAPTURED_FIRST = """
 import sys
 sys.path.insert(0, {root!r})
