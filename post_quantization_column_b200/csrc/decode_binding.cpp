@@ -4,7 +4,9 @@
 // marshalling of their 20 to 40 arguments took longer (9 to 14 us a call) than the kernels; here a
 // call takes what its checks, the output's allocation and the launch take. Arguments are marshalled
 // and checked only: all device work is in libawqsearch.so. Each function works on the current
-// stream and returns the output tensors, or the library's status as an int when that is not OK.
+// stream and returns the output tensors, or the library's status as an int when that is not OK. Once
+// its Python arguments are taken it runs without the interpreter lock, as ctypes does: an allocation
+// or a launch may wait for the device.
 #include <ATen/cuda/CUDAContext.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/AutogradState.h>
@@ -151,6 +153,18 @@ awq_paged_cache cache_of(const Tensor& k, const Tensor& v, const Tensor& table, 
   return c;
 }
 
+// Gives the interpreter lock up while it lives.
+class Unlocked {
+ public:
+  Unlocked() : thread_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(thread_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* thread_;
+};
+
 PyObject* result(int status, const Tensor& out) {
   return status == AWQ_OK ? THPVariable_Wrap(out) : PyLong_FromLong(status);
 }
@@ -174,42 +188,45 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded(n, 6, [&]() -> PyObject* {
     Tensor X = tensor(args[0], "X must be a tensor"), weight = tensor(args[1], "weight must be a tensor");
     Tensor residual = maybe(args[3], "residual must be a tensor"), into = maybe(args[4], "residual_out must be a tensor");
+    const at::ScalarType out_type = dtype_of(args[5]);
     const double eps = PyFloat_AsDouble(args[2]);
     if (PyErr_Occurred()) return nullptr;
-    value_check(X.is_cuda(), "rms_norm() takes CUDA tensors");
-    const at::Device device = X.device();
-    value_check(X.dim() == 2 && weight.dim() == 1 && weight.size(0) == X.size(1), "X must be (M, K) and weight (K,)");
-    const int xc = dtype_code(X.scalar_type()), wc = dtype_code(weight.scalar_type());
-    type_check(plain_float(xc) && plain_float(wc), "X and weight must be float32, float16 or bfloat16");
-    const at::ScalarType out_type = dtype_of(args[5]);
-    const int oc = dtype_code(out_type);
-    type_check(oc >= 0, "out_dtype must be float32, float16, bfloat16 or float8_e4m3fn");
-    for (const Tensor* t : std::initializer_list<const Tensor*>{&X, &weight, &residual, &into}) on_device(*t, device);
-    const int64_t M = X.size(0), K = X.size(1);
-    if (X.stride(1) != 1) X = X.contiguous();
-    weight = weight.contiguous();
-    int rc = 0;
-    int64_t r_stride = K, ro_stride = K;
-    if (residual.defined()) {
-      if (!into.defined()) into = residual;
-      rc = dtype_code(residual.scalar_type());
-      value_check(residual.sizes() == X.sizes() && plain_float(rc), "residual must be (M, K) in float32, float16 or bfloat16");
-      value_check(into.sizes() == X.sizes() && into.scalar_type() == residual.scalar_type() && (K <= 1 || into.stride(1) == 1),
-                  "residual_out must be (M, K) of the residual's dtype with contiguous rows");
-      if (residual.stride(1) != 1) residual = residual.contiguous();
-      if (M > 1) {
-        r_stride = residual.stride(0);
-        ro_stride = into.stride(0);
+    Tensor out, scales;
+    const int st = [&] {
+      Unlocked unlocked;
+      value_check(X.is_cuda(), "rms_norm() takes CUDA tensors");
+      const at::Device device = X.device();
+      value_check(X.dim() == 2 && weight.dim() == 1 && weight.size(0) == X.size(1), "X must be (M, K) and weight (K,)");
+      const int xc = dtype_code(X.scalar_type()), wc = dtype_code(weight.scalar_type()), oc = dtype_code(out_type);
+      type_check(plain_float(xc) && plain_float(wc), "X and weight must be float32, float16 or bfloat16");
+      type_check(oc >= 0, "out_dtype must be float32, float16, bfloat16 or float8_e4m3fn");
+      for (const Tensor* t : std::initializer_list<const Tensor*>{&X, &weight, &residual, &into}) on_device(*t, device);
+      const int64_t M = X.size(0), K = X.size(1);
+      if (X.stride(1) != 1) X = X.contiguous();
+      weight = weight.contiguous();
+      int rc = 0;
+      int64_t r_stride = K, ro_stride = K;
+      if (residual.defined()) {
+        if (!into.defined()) into = residual;
+        rc = dtype_code(residual.scalar_type());
+        value_check(residual.sizes() == X.sizes() && plain_float(rc), "residual must be (M, K) in float32, float16 or bfloat16");
+        value_check(into.sizes() == X.sizes() && into.scalar_type() == residual.scalar_type() && (K <= 1 || into.stride(1) == 1),
+                    "residual_out must be (M, K) of the residual's dtype with contiguous rows");
+        if (residual.stride(1) != 1) residual = residual.contiguous();
+        if (M > 1) {
+          r_stride = residual.stride(0);
+          ro_stride = into.stride(0);
+        }
+      } else {
+        value_check(!into.defined(), "residual_out comes with a residual");
       }
-    } else {
-      value_check(!into.defined(), "residual_out comes with a residual");
-    }
-    Tensor out = empty({M, K}, out_type, device), scales;
-    if (oc == AWQ_DTYPE_E4M3) scales = empty({M}, at::kFloat, device);
-    const int st = awq_rms_norm_on(device.index(), X.data_ptr(), xc, X.stride(0), residual.defined() ? residual.data_ptr() : nullptr,
-                                   rc, r_stride, into.defined() ? into.data_ptr() : nullptr, ro_stride, weight.data_ptr(), wc, M,
-                                   K, static_cast<float>(eps), out.data_ptr(), oc,
-                                   scales.defined() ? scales.data_ptr<float>() : nullptr, current_stream(device));
+      out = empty({M, K}, out_type, device);
+      if (oc == AWQ_DTYPE_E4M3) scales = empty({M}, at::kFloat, device);
+      return awq_rms_norm_on(device.index(), X.data_ptr(), xc, X.stride(0), residual.defined() ? residual.data_ptr() : nullptr, rc,
+                             r_stride, into.defined() ? into.data_ptr() : nullptr, ro_stride, weight.data_ptr(), wc, M, K,
+                             static_cast<float>(eps), out.data_ptr(), oc, scales.defined() ? scales.data_ptr<float>() : nullptr,
+                             current_stream(device));
+    }();
     if (st == AWQ_OK) written(into);
     if (st != AWQ_OK || !scales.defined()) return result(st, out);
     return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(scales));
@@ -229,40 +246,44 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int interleaved = PyObject_IsTrue(args[9]);
     const double magnitude = PyFloat_AsDouble(args[10]);
     if (PyErr_Occurred()) return nullptr;
-    value_check(k.is_cuda(), "kv_append() takes CUDA tensors");
-    const at::Device device = k.device();
-    for (const Tensor* t : std::initializer_list<const Tensor*>{&q, &k, &v, &k_cache, &v_cache, &table, &positions, &freqs, &seqs, &k_scale, &v_scale}) on_device(*t, device);
-    const awq_paged_cache cache = cache_of(k_cache, v_cache, table, k_scale, v_scale);
-    k = rows16(k, cache.heads, cache.head_dim, "k must be (tokens, heads, head_dim) of the cache's heads");
-    v = rows16(v, cache.heads, cache.head_dim, "v must be (tokens, heads, head_dim) of the cache's heads");
-    const int64_t T = k.size(0);
-    const int in = dtype_code(k.scalar_type());
-    const char* same = "q, k and v must share T and a dtype of float32, float16 or bfloat16";
-    value_check(v.size(0) == T && v.scalar_type() == k.scalar_type() && plain_float(in), same);
-    const at::ScalarType q_type = args[13] != Py_None ? dtype_of(args[13])
-                                                      : (cache.dtype == AWQ_DTYPE_E4M3 ? at::kHalf : k_cache.scalar_type());
-    type_check(half_float(dtype_code(q_type)), "q_dtype must be float16 or bfloat16");
+    const bool asked = args[13] != Py_None;
+    const at::ScalarType asked_type = asked ? dtype_of(args[13]) : at::kHalf;
     Tensor out;
-    int64_t Hq = 0;
-    if (q.defined()) {
-      q = rows16(q, -1, cache.head_dim, "q must be (T, Hq, head_dim)");
-      Hq = q.size(1);
-      value_check(q.size(0) == T && q.scalar_type() == k.scalar_type(), same);
-      out = empty({T, Hq, cache.head_dim}, q_type, device);
-    }
-    value_check(is_vector(positions, at::kInt, T) && (!seqs.defined() || is_vector(seqs, at::kInt, T)),
-                "positions and seqs must be (T,) contiguous int32");
-    if (freqs.defined())
-      value_check(freqs.dim() == 1 && is_vector(freqs, at::kDouble, freqs.size(0)),
-                  "freqs must be a contiguous float64 vector (rope_frequencies)");
-    const int64_t rot = freqs.defined() ? 2 * freqs.size(0) : 0;
-    value_check(rot <= cache.head_dim, "freqs must have at most head_dim / 2 entries");
-    const int st = awq_kv_append_on(
-        device.index(), Hq ? q.data_ptr() : nullptr, Hq ? q.stride(0) : 0, Hq ? q.stride(1) : 0, k.data_ptr(), k.stride(0), k.stride(1),
-        v.data_ptr(), v.stride(0), v.stride(1), in, T, static_cast<int>(Hq), Hq ? out.data_ptr() : nullptr, dtype_code(q_type),
-        positions.data_ptr<int32_t>(), seqs.defined() ? seqs.data_ptr<int32_t>() : nullptr,
-        rot ? freqs.data_ptr<double>() : nullptr, static_cast<int>(rot), interleaved, static_cast<float>(magnitude), &cache,
-        status_word(status, device), current_stream(device));
+    const int st = [&] {
+      Unlocked unlocked;
+      value_check(k.is_cuda(), "kv_append() takes CUDA tensors");
+      const at::Device device = k.device();
+      for (const Tensor* t : std::initializer_list<const Tensor*>{&q, &k, &v, &k_cache, &v_cache, &table, &positions, &freqs, &seqs, &k_scale, &v_scale}) on_device(*t, device);
+      const awq_paged_cache cache = cache_of(k_cache, v_cache, table, k_scale, v_scale);
+      k = rows16(k, cache.heads, cache.head_dim, "k must be (tokens, heads, head_dim) of the cache's heads");
+      v = rows16(v, cache.heads, cache.head_dim, "v must be (tokens, heads, head_dim) of the cache's heads");
+      const int64_t T = k.size(0);
+      const int in = dtype_code(k.scalar_type());
+      const char* same = "q, k and v must share T and a dtype of float32, float16 or bfloat16";
+      value_check(v.size(0) == T && v.scalar_type() == k.scalar_type() && plain_float(in), same);
+      const at::ScalarType q_type = asked ? asked_type : (cache.dtype == AWQ_DTYPE_E4M3 ? at::kHalf : k_cache.scalar_type());
+      type_check(half_float(dtype_code(q_type)), "q_dtype must be float16 or bfloat16");
+      int64_t Hq = 0;
+      if (q.defined()) {
+        q = rows16(q, -1, cache.head_dim, "q must be (T, Hq, head_dim)");
+        Hq = q.size(1);
+        value_check(q.size(0) == T && q.scalar_type() == k.scalar_type(), same);
+        out = empty({T, Hq, cache.head_dim}, q_type, device);
+      }
+      value_check(is_vector(positions, at::kInt, T) && (!seqs.defined() || is_vector(seqs, at::kInt, T)),
+                  "positions and seqs must be (T,) contiguous int32");
+      if (freqs.defined())
+        value_check(freqs.dim() == 1 && is_vector(freqs, at::kDouble, freqs.size(0)),
+                    "freqs must be a contiguous float64 vector (rope_frequencies)");
+      const int64_t rot = freqs.defined() ? 2 * freqs.size(0) : 0;
+      value_check(rot <= cache.head_dim, "freqs must have at most head_dim / 2 entries");
+      return awq_kv_append_on(
+          device.index(), Hq ? q.data_ptr() : nullptr, Hq ? q.stride(0) : 0, Hq ? q.stride(1) : 0, k.data_ptr(), k.stride(0), k.stride(1),
+          v.data_ptr(), v.stride(0), v.stride(1), in, T, static_cast<int>(Hq), Hq ? out.data_ptr() : nullptr, dtype_code(q_type),
+          positions.data_ptr<int32_t>(), seqs.defined() ? seqs.data_ptr<int32_t>() : nullptr,
+          rot ? freqs.data_ptr<double>() : nullptr, static_cast<int>(rot), interleaved, static_cast<float>(magnitude), &cache,
+          status_word(status, device), current_stream(device));
+    }();
     if (st != AWQ_OK) return PyLong_FromLong(st);
     written(k_cache);
     written(v_cache);
@@ -279,29 +300,35 @@ PyObject* paged_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const Tensor &table = tensor(args[3], "block_table must be a tensor"), &lengths = tensor(args[4], "lengths must be a tensor");
     const Tensor k_scale = maybe(args[6], "k_scale must be a tensor"), v_scale = maybe(args[7], "v_scale must be a tensor");
     const Tensor status = maybe(args[8], "status must be a tensor");
-    value_check(q.is_cuda(), "paged_attention() takes CUDA tensors");
-    const at::Device device = q.device();
-    for (const Tensor* t : std::initializer_list<const Tensor*>{&q, &k_cache, &v_cache, &table, &lengths, &k_scale, &v_scale}) on_device(*t, device);
-    const int qc = dtype_code(q.scalar_type());
-    value_check(q.dim() == 3 && half_float(qc), "q must be (sequences, Hq, head_dim) float16 or bfloat16");
-    const int64_t B = q.size(0), Hq = q.size(1), D = q.size(2);
-    const double scale = args[5] == Py_None ? 1.0 / std::sqrt(static_cast<double>(std::max<int64_t>(D, 1))) : PyFloat_AsDouble(args[5]);
+    const bool asked = args[5] != Py_None;
+    const double asked_scale = asked ? PyFloat_AsDouble(args[5]) : 0.0;
     if (PyErr_Occurred()) return nullptr;
-    Tensor out = empty({B, Hq, D}, q.scalar_type(), device);
-    if (B == 0) return THPVariable_Wrap(out);
-    const awq_paged_cache cache = cache_of(k_cache, v_cache, table, k_scale, v_scale);
-    value_check(cache.n_seqs == B, "block_table needs one row per sequence");
-    value_check(D == cache.head_dim && cache.heads > 0 && Hq % cache.heads == 0,
-                "q's head_dim must be the cache's, and the cache's heads must divide q's");
-    type_check(cache.dtype == qc || cache.dtype == AWQ_DTYPE_E4M3, "a 16-bit cache and its queries share a dtype");
-    value_check(is_vector(lengths, at::kInt, B), "lengths must be (sequences,) contiguous int32");
-    q = rows16(q, Hq, D, "q must be (sequences, Hq, head_dim)");
-    const int64_t bytes = awq_paged_attention_workspace(static_cast<int>(Hq), static_cast<int>(cache.heads), static_cast<int>(D),
-                                                        static_cast<int>(cache.dtype));
-    const Tensor workspace = empty({bytes}, at::kByte, device);
-    const int st = awq_paged_attention_on(device.index(), q.data_ptr(), q.stride(0), q.stride(1), qc, static_cast<int>(Hq), &cache,
-                                          lengths.data_ptr<int32_t>(), static_cast<float>(scale), out.data_ptr(),
-                                          workspace.data_ptr(), bytes, status_word(status, device), current_stream(device));
+    Tensor out;
+    const int st = [&]() -> int {
+      Unlocked unlocked;
+      value_check(q.is_cuda(), "paged_attention() takes CUDA tensors");
+      const at::Device device = q.device();
+      for (const Tensor* t : std::initializer_list<const Tensor*>{&q, &k_cache, &v_cache, &table, &lengths, &k_scale, &v_scale}) on_device(*t, device);
+      const int qc = dtype_code(q.scalar_type());
+      value_check(q.dim() == 3 && half_float(qc), "q must be (sequences, Hq, head_dim) float16 or bfloat16");
+      const int64_t B = q.size(0), Hq = q.size(1), D = q.size(2);
+      const double scale = asked ? asked_scale : 1.0 / std::sqrt(static_cast<double>(std::max<int64_t>(D, 1)));
+      out = empty({B, Hq, D}, q.scalar_type(), device);
+      if (B == 0) return AWQ_OK;
+      const awq_paged_cache cache = cache_of(k_cache, v_cache, table, k_scale, v_scale);
+      value_check(cache.n_seqs == B, "block_table needs one row per sequence");
+      value_check(D == cache.head_dim && cache.heads > 0 && Hq % cache.heads == 0,
+                  "q's head_dim must be the cache's, and the cache's heads must divide q's");
+      type_check(cache.dtype == qc || cache.dtype == AWQ_DTYPE_E4M3, "a 16-bit cache and its queries share a dtype");
+      value_check(is_vector(lengths, at::kInt, B), "lengths must be (sequences,) contiguous int32");
+      q = rows16(q, Hq, D, "q must be (sequences, Hq, head_dim)");
+      const int64_t bytes = awq_paged_attention_workspace(static_cast<int>(Hq), static_cast<int>(cache.heads), static_cast<int>(D),
+                                                          static_cast<int>(cache.dtype));
+      const Tensor workspace = empty({bytes}, at::kByte, device);
+      return awq_paged_attention_on(device.index(), q.data_ptr(), q.stride(0), q.stride(1), qc, static_cast<int>(Hq), &cache,
+                                    lengths.data_ptr<int32_t>(), static_cast<float>(scale), out.data_ptr(), workspace.data_ptr(),
+                                    bytes, status_word(status, device), current_stream(device));
+    }();
     return result(st, out);
   });
 }

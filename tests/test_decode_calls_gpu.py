@@ -147,6 +147,38 @@ def test_forward_mode_tangents_are_refused():
         awq.rms_norm(X, w)
 
 
+def test_other_threads_run_while_a_call_waits_for_the_queue():
+    """A call that finds the launch queue full waits without the interpreter lock."""
+    import threading
+    import time
+    X, w = _randn(1, 64, seed=1), _randn(64, seed=2)
+    awq.rms_norm(X, w)
+    torch.cuda.synchronize()
+    gaps, stop = [0.0], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+
+    other = threading.Thread(target=tick)
+    other.start()
+    time.sleep(0.05)
+    torch.cuda._sleep(2_000_000_000)   # about 1 s
+    start = time.perf_counter()
+    for _ in range(4000):
+        awq.rms_norm(X, w)
+    took = time.perf_counter() - start
+    stop.set()
+    other.join()
+    torch.cuda.synchronize()
+    if took > 0.5:   # the queue was full, and the calls waited
+        assert max(gaps) < took / 2, (max(gaps), took)
+
+
 _CAPTURED_FIRST = """
 import sys
 sys.path.insert(0, {root!r})
