@@ -719,7 +719,10 @@ def _on_stream(stream, call, args):
 
 def check_status(status: torch.Tensor) -> None:
     """Raises AwqError if a decode-step operator given this `status` reported an error (waits
-    for the device; a pinned host word is read as it is: synchronize its stream first)."""
+    for the device, whichever stream the operator is on; a pinned host word is read as it is:
+    synchronize its stream first)."""
+    if status.is_cuda:
+        torch.cuda.synchronize(status.device)
     st = int(status.reshape(-1)[0])
     if st != 0:
         raise AwqError(st, "a block table names no place of the cache, or a length or position lies beyond the table")

@@ -107,6 +107,20 @@ def _decode_inputs():
     return q, k, v, kc, vc, table, torch.tensor([4, 9], dtype=torch.int32, device="cuda")
 
 
+def test_status_of_a_call_on_another_stream():
+    """check_status waits for the device, whichever stream the reporting call is on."""
+    q, k, v, kc, vc, table, pos = _decode_inputs()
+    table.fill_(99)
+    status, side = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.cuda.Stream()
+    awq.paged_attention(q, kc, vc, table, pos + 1)   # what a first call loads is loaded
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)               # 0.2 s
+    awq.paged_attention(q, kc, vc, table, pos + 1, status=status, stream=side)
+    with pytest.raises(awq.AwqError):
+        awq.check_status(status)
+
+
 def test_tensors_that_autograd_saved_are_written_openly():
     """An in-place write of a tensor that a backward pass still needs makes that pass an error."""
     q, k, v, kc, vc, table, pos = _decode_inputs()
