@@ -208,7 +208,8 @@ int awq_profile_last(float* ms, int n);
 int64_t awq_profile_last_ticket(void);
 int awq_profile_collect(int64_t ticket, float* ms, int n);
 const char* awq_profile_phase_name(int phase);
-/* Kernel launches the last call made (all of them this library's own kernels). */
+/* Kernel launches that the calling thread's last call made (all of them this library's own
+ * kernels); in a thread that has made none, those of the last call of any thread. */
 int awq_last_launch_count(void);
 
 /* Testing hook for the bounded waits: mode 1 makes the loss GEMM's producer skip

@@ -35,7 +35,13 @@ std::mutex g_mu;
 std::unordered_map<int, cudaMemPool_t> g_pools;
 bool g_profile = false;
 float g_phase_ms[kNumPhases] = {0};
+// Launches of the last call: the calling thread's (-1: it has made none), and any thread's.
+thread_local int t_last_launches = -1;
 int g_last_launches = 0;
+void set_last_launches(int n) {
+  t_last_launches = n;
+  __atomic_store_n(&g_last_launches, n, __ATOMIC_RELAXED);
+}
 int g_fault_mode = 0;
 uint64_t g_timeout_ns = kDefaultTimeoutNs;
 
@@ -575,7 +581,7 @@ int search_device(const void* X, const void* W, int in_dtype, int64_t M, int64_t
     }
     if (status == AWQ_OK && e != cudaSuccess) status = cuda_error(e, where);
     if (!fixed) cudaFreeAsync(ws, s);
-    g_last_launches = launches;
+    set_last_launches(launches);
     return status;
   }
   int h_err = 0;
@@ -593,7 +599,7 @@ int search_device(const void* X, const void* W, int in_dtype, int64_t M, int64_t
   if (pinned) h_err = *pinned;
   if (status == AWQ_OK) {
     ev.collect();
-    g_last_launches = launches;
+    set_last_launches(launches);
     status = status_from_word(h_err);
   }
   return status;
@@ -639,7 +645,7 @@ bool decode_status_memory(const void* p, int dev) {
   return (at.type == cudaMemoryTypeDevice && at.device == dev) || at.type == cudaMemoryTypeManaged ||
          (at.type == cudaMemoryTypeHost && at.devicePointer == p);
 }
-void record_launch_count(int launches) { g_last_launches = launches; }
+void record_launch_count(int launches) { set_last_launches(launches); }
 
 int search_in_workspace(const void* X, const void* W, int in_dtype, int64_t M, int64_t K, int64_t N, int group,
                         int n_grid, float* out_scales, int32_t* out_codes, void* out_steps, void* out_zeros,
@@ -976,7 +982,7 @@ int awq_activation_statistic(const void* X, int in_dtype, int64_t M, int64_t K, 
   cudaError_t se = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_error(e, "statistic");
   if (se != cudaSuccess) return cuda_error(se, "stream synchronize");
-  g_last_launches = launches;
+  set_last_launches(launches);
   if (h_err & kErrNonfiniteX) return set_error(AWQ_ERR_NONFINITE, "non-finite value in X");
   return AWQ_OK;
 }
@@ -998,7 +1004,7 @@ int awq_candidate_scales(const float* a, int64_t K, int n_grid, float* out_S, aw
   cudaError_t se = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_error(e, "scales");
   if (se != cudaSuccess) return cuda_error(se, "stream synchronize");
-  g_last_launches = launches;
+  set_last_launches(launches);
   return AWQ_OK;
 }
 
@@ -1035,7 +1041,7 @@ int awq_qdq_candidates(const void* W, int in_dtype, int64_t K, int64_t N, int gr
   cudaError_t se = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_error(e, "qdq");
   if (se != cudaSuccess) return cuda_error(se, "stream synchronize");
-  g_last_launches = launches;
+  set_last_launches(launches);
   if (h_err & kErrNonfiniteW) return set_error(AWQ_ERR_NONFINITE, "non-finite value in W");
   return AWQ_OK;
 }
@@ -1107,7 +1113,7 @@ int awq_clip_search(const void* X, const void* W, int in_dtype, const float* sca
   if (e != cudaSuccess) return cuda_error(e, "clipping search");
   if (se != cudaSuccess) return cuda_error(se, "stream synchronize");
   if (pinned) h_err = *pinned;
-  g_last_launches = launches;
+  set_last_launches(launches);
   if (a.ev) {
     cudaEventElapsedTime(&g_clip_ms[0], a.ev[0], a.ev[1]);
     cudaEventElapsedTime(&g_clip_ms[1], a.ev[1], a.ev[2]);
@@ -1185,7 +1191,7 @@ int awq_w4a16_matmul(const void* A, const int32_t* codes, const void* steps, con
     g_w4a16_profiled = ev != nullptr;
     cudaFreeAsync(ws, s);
     if (e != cudaSuccess) return cuda_error(e, "W4A16 GEMV");
-    g_last_launches = launches;
+    set_last_launches(launches);
     return AWQ_OK;
   }
   int* pinned = pinned_status_word(dev);
@@ -1235,7 +1241,7 @@ int awq_w4a16_matmul(const void* A, const int32_t* codes, const void* steps, con
   if (status == AWQ_OK && se != cudaSuccess) status = cuda_error(se, "stream synchronize");
   if (pinned) h_err = *pinned;
   if (status == AWQ_OK) {
-    g_last_launches = launches;
+    set_last_launches(launches);
     if (h_err & kErrTimeout) status = set_error(AWQ_ERR_TIMEOUT, "a bounded wait in the W4A16 GEMM ran out");
     else if (h_err) status = set_error(AWQ_ERR_CUDA, "device status word " + std::to_string(h_err));
   }
@@ -1261,7 +1267,7 @@ int awq_w4a16_repack(const int32_t* codes, int64_t K, int64_t N, int32_t* out_pa
   cudaError_t se = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_error(e, "repack");
   if (se != cudaSuccess) return cuda_error(se, "stream synchronize");
-  g_last_launches = launches;
+  set_last_launches(launches);
   return AWQ_OK;
 }
 
@@ -1308,7 +1314,7 @@ int awq_w4a16_matmul_packed(const void* A, const int32_t* packed, const void* st
   g_w4a16_profiled = ev != nullptr;
   cudaFreeAsync(ws, s);
   if (e != cudaSuccess) return cuda_error(e, "W4A16 GEMV (repacked)");
-  g_last_launches = launches;
+  set_last_launches(launches);
   return AWQ_OK;
 }
 
@@ -1342,7 +1348,7 @@ int awq_w4a16_dequant(const int32_t* codes, const void* steps, const void* zeros
   cudaError_t se = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_error(e, "W4A16 dequantization");
   if (se != cudaSuccess) return cuda_error(se, "stream synchronize");
-  g_last_launches = launches;
+  set_last_launches(launches);
   return AWQ_OK;
 }
 
@@ -1573,7 +1579,7 @@ int awq_search_mlp(const void* X, const void* W_gu, const void* W_down, int in_d
   if (status == AWQ_OK && se != cudaSuccess) status = cuda_error(se, "stream synchronize");
   if (pinned) h_err = *pinned;
   if (status == AWQ_OK) {
-    g_last_launches = launches;
+    set_last_launches(launches);
     if (h_err & kErrTimeout)
       status = set_error(AWQ_ERR_TIMEOUT, "a bounded wait in a block GEMM ran out");
     else if (h_err & (kErrNonfiniteX | kErrNonfiniteW))
@@ -1820,7 +1826,7 @@ int awq_search_attn(const void* X, const void* W_qkv, int in_dtype, int64_t M, i
   if (status == AWQ_OK && se != cudaSuccess) status = cuda_error(se, "stream synchronize");
   if (pinned) h_err = *pinned;
   if (status == AWQ_OK) {
-    g_last_launches = launches;
+    set_last_launches(launches);
     if (ev)
       for (int i = 0; i < kAttnPhases; ++i) cudaEventElapsedTime(&g_attn_ms[i], ev[i], ev[i + 1]);
     status = status_from_word(h_err);
@@ -1942,7 +1948,9 @@ const char* awq_profile_phase_name(int phase) {
   return (phase >= 0 && phase < kNumPhases) ? kPhaseNames[phase] : "";
 }
 
-int awq_last_launch_count(void) { return g_last_launches; }
+int awq_last_launch_count(void) {
+  return t_last_launches >= 0 ? t_last_launches : __atomic_load_n(&g_last_launches, __ATOMIC_RELAXED);
+}
 
 int awq_debug_set_fault(int mode, int64_t timeout_ns) {
   if (mode != 0 && mode != 1 && mode != 3) return set_error(AWQ_ERR_INVALID_ARG, "fault mode must be 0, 1 or 3");

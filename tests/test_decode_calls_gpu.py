@@ -193,6 +193,25 @@ def test_other_threads_run_while_a_call_waits_for_the_queue():
         assert max(gaps) < took / 2, (max(gaps), took)
 
 
+def test_launch_counts_are_the_calling_thread_s():
+    import threading
+    X, W = _randn(128, 256, seed=1), _randn(256, 256, seed=2)
+    awq.search(X, W, n_grid=4)
+    made = awq.last_launch_count()
+    seen = []
+
+    def work():
+        x, w = _randn(4, 64, seed=1), _randn(64, seed=2)
+        for _ in range(20):
+            awq.rms_norm(x, w)
+        seen.append(awq.last_launch_count())
+
+    other = threading.Thread(target=work)
+    other.start()
+    other.join()
+    assert made > 1 and seen == [1] and awq.last_launch_count() == made
+
+
 _CAPTURED_FIRST = """
 import sys
 sys.path.insert(0, {root!r})
