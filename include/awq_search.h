@@ -436,7 +436,8 @@ typedef struct awq_paged_cache {
  * sequence, position or page lies outside the table or the cache is not appended, its q_out
  * is still written, and *status (device or pinned host memory, may be NULL) is set to
  * AWQ_ERR_INVALID_ARG; *status is never cleared, and other memory than these is refused. Two tokens of a call must not name one
- * place of the cache: what that place then holds is undefined. */
+ * place of the cache: what that place then holds is undefined. Of the cache's strides (of dims above
+ * one) each must step over the whole of what steps less, so that its rows lie apart. */
 int awq_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
                   int64_t k_token_stride, int64_t k_head_stride, const void* v,
                   int64_t v_token_stride, int64_t v_head_stride, int in_dtype, int64_t T, int Hq,

@@ -5,7 +5,9 @@
 #include "decode_kernels.h"
 
 #include <algorithm>
+#include <array>
 #include <cmath>
+#include <utility>
 
 namespace {
 
@@ -98,6 +100,19 @@ int take_cache(const awq_paged_cache* in, PagedCache* out) {
   out->max_pages = in->max_pages;
   out->table_stride = in->table_stride;
   return AWQ_OK;
+}
+
+// Whether no two rows of the cache overlap: each of pages, slots and heads steps over the whole of
+// what steps less, as in any order of the three and any part of such a cache.
+bool rows_apart(const PagedCache& c) {
+  std::array<std::pair<int64_t, int64_t>, 3> dims{{{c.page_stride, c.num_pages - 1}, {c.slot_stride, c.page_size - 1}, {c.head_stride, c.heads - 1}}};
+  std::sort(std::begin(dims), std::end(dims));
+  int64_t span = c.head_dim;  // the sum is within what take_cache has checked
+  for (const auto& [stride, steps] : dims) {
+    if (steps > 0 && stride < span) return false;
+    span += stride * steps;
+  }
+  return true;
 }
 
 }  // namespace
@@ -237,10 +252,7 @@ int awq_kv_append_on(int device, const void* q, int64_t q_token_stride, int64_t 
     return decode_error(AWQ_ERR_INVALID_ARG, "strides must not be negative");
   if (std::max(q_head_stride, std::max(k_head_stride, v_head_stride)) > kIntMax / 4)
     return decode_error(AWQ_ERR_SHAPE, "the head strides of q, k and v must be below 2^29");
-  const int64_t D = a.c.head_dim;
-  if ((a.c.num_pages > 1 && a.c.page_stride < D) || (a.c.page_size > 1 && a.c.slot_stride < D) ||
-      (a.c.heads > 1 && a.c.head_stride < D))
-    return decode_error(AWQ_ERR_INVALID_ARG, "rows of a cache that is written must not overlap");
+  if (!rows_apart(a.c)) return decode_error(AWQ_ERR_INVALID_ARG, "rows of a cache that is written must not overlap");
   if (!aligned(positions, 4) || !aligned(seqs, 4) || !aligned(freqs, 8) || !aligned(status, 4))
     return decode_error(AWQ_ERR_INVALID_ARG, "positions, seqs, freqs or status is misaligned");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
