@@ -377,7 +377,7 @@ int awq_w4a16_dequant(const int32_t* codes, const void* steps, const void* zeros
  *   y[m][k] = h[m][k] weight[k] / sqrt(mean_k h[m][k]^2 + eps)   (statistics in fp32, of the
  *   unrounded h; rounded once to out_dtype)
  * X [M][K], residual and residual_out [M][K] (may be NULL together; residual_out may be
- * `residual` itself; otherwise it, and `out`, meet no row of another argument) and weight [K] each hold
+ * `residual` itself; otherwise it, `out` and out_scales meet no row of another argument) and weight [K] each hold
  * AWQ_DTYPE_F32, _F16 or _BF16; rows x_stride, r_stride and ro_stride apart. out [M][K]
  * contiguous holds one of these types, or AWQ_DTYPE_E4M3: out_scales[m] = max_k |y| / 448 (1
  * where that is zero) and out = e4m3(y / out_scales[m]); a row with a NaN or an infinity has
@@ -428,7 +428,8 @@ typedef struct awq_paged_cache {
  * q_out[t] = rotated q[t] ([T][Hq][D] contiguous, AWQ_DTYPE_F16 or _BF16) and the rotated k[t]
  * and v[t] to the cache (e4m3: e4m3(x / scale), saturating at 448). q [T][Hq][D], k and v
  * [T][heads][D] hold in_dtype (F32, F16 or BF16), rows 16-byte aligned and head strides below 2^29,
- * e.g. the three parts of one QKV product. Hq may be 0 (q, q_out unused). The pairs of dims (i, i + rotary_dim / 2),
+ * e.g. the three parts of one QKV product. q_out may be q itself (contiguous, of one type) but
+ * overlap nothing else. Hq may be 0 (q, q_out unused). The pairs of dims (i, i + rotary_dim / 2),
  * or (2 i, 2 i + 1) if `interleaved`, i < rotary_dim / 2, are turned by positions[t] * freqs[i]
  * (DEVICE doubles; the product is taken in fp64) and multiplied by `magnitude`; dims from
  * rotary_dim (a multiple of 16, at most D; 0 turns nothing) on are copied. A negative
@@ -456,7 +457,8 @@ int awq_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, 
  * and sets *status (device or pinned host memory, may be NULL, never cleared) to
  * AWQ_ERR_INVALID_ARG. `workspace`: at least
  * awq_paged_attention_workspace bytes of device memory (0 on bad arguments), 16-byte
- * aligned, needing no initialisation; calls that may overlap need one each. */
+ * aligned, needing no initialisation; calls that may overlap need one each. `out` may be q itself
+ * (contiguous); it and the work space overlap nothing else. */
 int64_t awq_paged_attention_workspace(int Hq, int Hkv, int head_dim, int cache_dtype);
 int awq_paged_attention(const void* q, int64_t q_seq_stride, int64_t q_head_stride, int q_dtype,
                         int Hq, const awq_paged_cache* cache, const int32_t* lengths, float scale,

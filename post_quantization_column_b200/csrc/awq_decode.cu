@@ -32,6 +32,22 @@ bool ranges_meet(const void* a, int64_t sa, int64_t wa, const void* b, int64_t s
   return d < wa || d + wb > sa;
 }
 
+// The bytes from a tensor's first to its last value: `n` rows `stride` bytes apart, of `m` parts `part`
+// bytes apart, each `bytes` long.
+struct Extent {
+  uintptr_t from;
+  unsigned __int128 to;
+};
+Extent extent(const void* p, int64_t n, int64_t stride, int64_t m, int64_t part, int64_t bytes) {
+  const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+  return {from, from + static_cast<unsigned __int128>(n - 1) * stride + static_cast<unsigned __int128>(m - 1) * part + bytes};
+}
+Extent extent(const PagedCache& c, const void* p) {
+  const int64_t b = type_bytes(c.type);
+  return extent(p, c.num_pages, c.page_stride * b, c.page_size, c.slot_stride * b, ((c.heads - 1) * c.head_stride + c.head_dim) * b);
+}
+bool meet(const Extent& a, const Extent& b) { return a.from < b.to && b.from < a.to; }
+
 constexpr int kAsk = -1;  // the device of the call is asked of its pointers
 
 // Makes the device of the call current: the caller's, which owns all its pointers (the Python
@@ -151,6 +167,13 @@ int awq_rms_norm_on(int device, const void* X, int x_dtype, int64_t x_stride, co
       (residual && (ranges_meet(residual, r_stride * rb, K * rb, out, K * ob, K * ob, M) ||
                     ranges_meet(residual_out, ro_stride * rb, K * rb, out, K * ob, K * ob, M))))
     return decode_error(AWQ_ERR_INVALID_ARG, "out must not overlap another argument");
+  if (out_dtype == kTypeE4m3) {
+    const Extent to = extent(out_scales, M, 4, 1, 0, 4);
+    if (meet(to, extent(X, M, x_stride * xb, 1, 0, K * xb)) || meet(to, extent(weight, 1, 0, 1, 0, K * wb)) ||
+        meet(to, extent(out, M, K, 1, 0, K)) ||
+        (residual && (meet(to, extent(residual, M, r_stride * rb, 1, 0, K * rb)) || meet(to, extent(residual_out, M, ro_stride * rb, 1, 0, K * rb)))))
+      return decode_error(AWQ_ERR_INVALID_ARG, "out_scales must not overlap another argument");
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DeviceRestore restore_device;
   const void* ptrs[] = {X, residual, residual_out, weight, out, out_dtype == kTypeE4m3 ? out_scales : nullptr};
@@ -255,6 +278,16 @@ int awq_kv_append_on(int device, const void* q, int64_t q_token_stride, int64_t 
   if (!rows_apart(a.c)) return decode_error(AWQ_ERR_INVALID_ARG, "rows of a cache that is written must not overlap");
   if (!aligned(positions, 4) || !aligned(seqs, 4) || !aligned(freqs, 8) || !aligned(status, 4))
     return decode_error(AWQ_ERR_INVALID_ARG, "positions, seqs, freqs or status is misaligned");
+  if (Hq > 0) {  // every unit of q is read and written by one thread, so that q_out may be q
+    const int64_t D = a.c.head_dim, b = type_bytes(in_dtype);
+    const Extent to = extent(q_out, T, Hq * D * 2, Hq, D * 2, D * 2);
+    const bool same = q_out == q && in_dtype == q_dtype && (T == 1 || q_token_stride == Hq * D) && (Hq == 1 || q_head_stride == D);
+    if ((!same && meet(to, extent(q, T, q_token_stride * b, Hq, q_head_stride * b, D * b))) ||
+        meet(to, extent(k, T, k_token_stride * b, a.c.heads, k_head_stride * b, D * b)) ||
+        meet(to, extent(v, T, v_token_stride * b, a.c.heads, v_head_stride * b, D * b)) || meet(to, extent(a.c, a.c.k)) ||
+        meet(to, extent(a.c, a.c.v)))
+      return decode_error(AWQ_ERR_INVALID_ARG, "q_out may be q itself but overlap nothing else");
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DeviceRestore restore_device;
   const void* ptrs[] = {k, v, positions, a.c.k, a.c.v, a.c.table, Hq > 0 ? q : nullptr, Hq > 0 ? q_out : nullptr, seqs,
@@ -325,6 +358,14 @@ int awq_paged_attention_on(int device, const void* q, int64_t q_seq_stride, int6
   if (!aligned(lengths, 4) || !aligned(status, 4)) return decode_error(AWQ_ERR_INVALID_ARG, "lengths or status is misaligned");
   if (workspace_bytes < awq_paged_attention_workspace(Hq, a.c.heads, a.c.head_dim, a.c.type))
     return decode_error(AWQ_ERR_INVALID_ARG, "the work space is smaller than awq_paged_attention_workspace says");
+  {  // a segment's queries are read before any of its outputs are written, so that out may be q
+    const int64_t B = a.c.seqs, D = a.c.head_dim;
+    const Extent to = extent(out, B, Hq * D * 2, Hq, D * 2, D * 2), from = extent(q, B, q_seq_stride * 2, Hq, q_head_stride * 2, D * 2),
+                 ws = extent(workspace, 1, 0, 1, 0, workspace_bytes), ck = extent(a.c, a.c.k), cv = extent(a.c, a.c.v);
+    const bool same = out == q && (B == 1 || q_seq_stride == Hq * D) && (Hq == 1 || q_head_stride == D);
+    if ((!same && meet(to, from)) || meet(to, ws) || meet(to, ck) || meet(to, cv) || meet(ws, from) || meet(ws, ck) || meet(ws, cv))
+      return decode_error(AWQ_ERR_INVALID_ARG, "out may be q itself; it and the work space overlap nothing else");
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DeviceRestore restore_device;
   const void* ptrs[] = {q, a.c.k, a.c.v, a.c.table, lengths, out, workspace, a.c.k_scale, a.c.v_scale};

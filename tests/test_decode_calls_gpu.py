@@ -74,6 +74,18 @@ def test_status_of_memory_that_a_kernel_cannot_reach_is_refused():
         assert int(status) == 0
 
 
+def test_rotated_queries_and_attention_in_place():
+    """q_out = q and out = q, as the header allows, against outputs of their own."""
+    for lens in ([5, 10], [16, 1]):
+        a, b = _Step(), _Step()
+        for s in (a, b):
+            s.lens.copy_(torch.tensor(lens))
+        assert a.append() == 0 and b.append(qo=b.q.data_ptr()) == 0
+        assert torch.equal(a.out, b.q) and all(torch.equal(x, y) for x, y in zip(a.caches, b.caches))
+        assert a.attend(out=a.q.data_ptr(), q=a.out.data_ptr()) == 0 and b.attend(out=b.q.data_ptr()) == 0
+        assert torch.equal(a.q, b.q)
+
+
 # ---- forms of the RMS norm that take rows too long for registers, value by value or in pairs ----------
 
 @pytest.mark.parametrize("K", [16385, 20001, 57343, 16386, 30002, 57342])
