@@ -277,6 +277,7 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
                     "freqs must be a contiguous float64 vector (rope_frequencies)");
       const int64_t rot = freqs.defined() ? 2 * freqs.size(0) : 0;
       value_check(rot <= cache.head_dim, "freqs must have at most head_dim / 2 entries");
+      if (T == 0) return static_cast<int>(AWQ_OK);  // whose table may be empty too
       return awq_kv_append_on(
           device.index(), Hq ? q.data_ptr() : nullptr, Hq ? q.stride(0) : 0, Hq ? q.stride(1) : 0, k.data_ptr(), k.stride(0), k.stride(1),
           v.data_ptr(), v.stride(0), v.stride(1), in, T, static_cast<int>(Hq), Hq ? out.data_ptr() : nullptr, dtype_code(q_type),

@@ -224,6 +224,16 @@ def test_launch_counts_are_the_calling_thread_s():
     assert made > 1 and seen == [1] and awq.last_launch_count() == made
 
 
+def test_a_step_without_tokens():
+    q, k, v, kc, vc, table, pos = _decode_inputs()
+    before = [kc.clone(), vc.clone()]
+    assert awq.kv_append(q[:0], k[:0], v[:0], kc, vc, table[:0], pos[:0]).shape == (0, 4, 128)
+    assert awq.kv_append(None, k[:0], v[:0], kc, vc, table[:0], pos[:0]) is None
+    assert awq.paged_attention(q[:0], kc, vc, table[:0], pos[:0]).shape == (0, 4, 128)
+    assert awq.rms_norm(q[:0].view(0, 128), torch.ones(128, device="cuda")).shape == (0, 128)
+    assert torch.equal(before[0], kc) and torch.equal(before[1], vc)
+
+
 _CAPTURED_FIRST = """
 import sys
 sys.path.insert(0, {root!r})
