@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libawqsearch.so")
 BINDING = os.path.join(PKG, "_decode.so")
 SOURCES = ["awq_api.cu", "k_statistic.cu", "k_qdq.cu", "k_loss_gemm.cu", "k_clip.cu", "k_w4a16.cu", "k_module.cu", "k_attn.cu", "awq_noalloc.cu", "gemm_policy.cu",
            "awq_decode.cu", "k_rmsnorm.cu", "k_rmsnorm_odd.cu", "k_kv_append.cu", "k_paged_attn.cu"]
-HEADERS = ["awq_device.cuh", "awq_kernels.h", "qdq_tile.cuh", "decode_kernels.h", "rmsnorm.cuh"]
+HEADERS = ["awq_device.cuh", "awq_kernels.h", "qdq_tile.cuh", "decode_kernels.h", "decode_entry.h", "rmsnorm.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 # IEEE division, square root and denormals everywhere: the QDQ must match the
@@ -86,7 +86,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
 
     import torch
     src = os.path.join(CSRC, "decode_binding.cpp")
-    if not (force or _stale(BINDING, [src, os.path.join(ROOT, "include", "awq_search.h")])):
+    if not (force or _stale(BINDING, [src, os.path.join(CSRC, "decode_entry.h"), os.path.join(ROOT, "include", "awq_search.h")])):
         return BINDING
     cxx = shutil.which("g++") or shutil.which("c++")
     if not cxx:

@@ -1,7 +1,7 @@
 // awq_decode.cu — the C ABI of the decode-step operators (declared in include/awq_search.h):
 // checks of the arguments, the device of the call, and the launches. All of it is
 // asynchronous on the caller's stream, allocates nothing and keeps nothing between calls.
-#include "../../include/awq_search.h"
+#include "decode_entry.h"
 #include "decode_kernels.h"
 
 #include <algorithm>

@@ -74,3 +74,14 @@ def test_outputs_that_overlap_other_arguments_are_refused():
             assert b"overlap" in awq.library().awq_last_error_message(), kw
         for kw in good:
             assert call(**kw) > 2, (kw, awq.library().awq_last_error_message())
+
+
+def test_entry_points_are_declared_in_one_place():
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(awq.__file__), "csrc")
+    for name in ("decode_binding.cpp", "awq_decode.cu"):
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        assert '#include "decode_entry.h"' in text
+        assert not re.search(r"^int awq_\w+_on\([^;{}]*\);$", text, re.M), name   # no declaration of its own
