@@ -21,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libawqsearch.so")
 BINDING = os.path.join(PKG, "_decode.so")
+BINDING_KEY = os.path.join(BUILD, "_decode.key")
 SOURCES = ["awq_api.cu", "k_statistic.cu", "k_qdq.cu", "k_loss_gemm.cu", "k_clip.cu", "k_w4a16.cu", "k_module.cu", "k_attn.cu", "awq_noalloc.cu", "gemm_policy.cu",
            "awq_decode.cu", "k_rmsnorm.cu", "k_rmsnorm_odd.cu", "k_kv_append.cu", "k_paged_attn.cu"]
 HEADERS = ["awq_device.cuh", "awq_kernels.h", "qdq_tile.cuh", "decode_kernels.h", "decode_entry.h", "rmsnorm.cuh"]
@@ -86,8 +87,6 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
 
     import torch
     src = os.path.join(CSRC, "decode_binding.cpp")
-    if not (force or _stale(BINDING, [src, os.path.join(CSRC, "decode_entry.h"), os.path.join(ROOT, "include", "awq_search.h")])):
-        return BINDING
     cxx = shutil.which("g++") or shutil.which("c++")
     if not cxx:
         raise RuntimeError("no C++ compiler found; it is required to build _decode.so")
@@ -98,9 +97,21 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
            "-L", PKG, "-lawqsearch", "-L", os.path.join(t, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
            "-Wl,-rpath,$ORIGIN"]
+    # what it was built for: another torch or Python needs another build
+    key = "\n".join([torch.__version__, sys.version, *cmd])
+    if os.path.exists(BINDING_KEY):
+        with open(BINDING_KEY) as f:
+            force = force or f.read() != key
+    else:
+        force = True
+    if not (force or _stale(BINDING, [src, os.path.join(CSRC, "decode_entry.h"), os.path.join(ROOT, "include", "awq_search.h")])):
+        return BINDING
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(BINDING_KEY, "w") as f:
+        f.write(key)
     return BINDING
 
 

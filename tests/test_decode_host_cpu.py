@@ -76,6 +76,44 @@ def test_outputs_that_overlap_other_arguments_are_refused():
             assert call(**kw) > 2, (kw, awq.library().awq_last_error_message())
 
 
+# ---- the build ---------------------------------------------------------------------------------------
+
+def _binding_builds(monkeypatch):
+    """What build_binding() would compile: its commands, which are not run."""
+    from post_quantization_column_b200 import build
+    ran = []
+    monkeypatch.setattr(build.subprocess, "run", lambda cmd, **kw: ran.append(cmd))
+    build.build_binding()
+    return ran
+
+
+def test_binding_is_built_again_when_what_it_was_built_for_changes(monkeypatch, tmp_path):
+    import os
+    import shutil
+
+    import torch
+    from post_quantization_column_b200 import build
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_decode.so"))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "BINDING_KEY", str(tmp_path / "_decode.key"))
+    csrc = tmp_path / "csrc"
+    csrc.mkdir()
+    for name in ("decode_binding.cpp", "decode_entry.h"):
+        shutil.copy(os.path.join(build.CSRC, name), csrc / name)
+    monkeypatch.setattr(build, "CSRC", str(csrc))
+    assert len(_binding_builds(monkeypatch)) == 1
+    (tmp_path / "_decode.so").write_bytes(b"")
+    assert _binding_builds(monkeypatch) == []
+    late = os.path.getmtime(tmp_path / "_decode.so") + 10
+    os.utime(csrc / "decode_entry.h", (late, late))
+    assert len(_binding_builds(monkeypatch)) == 1
+    os.utime(tmp_path / "_decode.so", (late + 10, late + 10))
+    assert _binding_builds(monkeypatch) == []
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    assert len(_binding_builds(monkeypatch)) == 1
+    assert _binding_builds(monkeypatch) == []
+
+
 def test_entry_points_are_declared_in_one_place():
     import os
     import re
