@@ -2,7 +2,8 @@
 
     python -m post_quantization_column_b200.build [--force] [--verbose]
 
-and _decode.so, the CPython binding of the decode-step operators, with the C++ compiler.
+and _decode.so, the CPython binding of the decode-step operators, with the C++ compiler where
+torch and Python's headers are there (programs that use the C library alone need neither).
 
 Objects go to ``post_quantization_column_b200/_build/`` (not committed); the shared
 library is written next to this file so the package finds it without installation.
@@ -77,8 +78,28 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-    build_binding(force, verbose)
+    lacking = _binding_lacks()
+    if lacking:
+        print(f"_decode.so is not built: {lacking}; libawqsearch.so does not need it", file=sys.stderr)
+    else:
+        build_binding(force, verbose)
     return LIB
+
+
+def _binding_lacks() -> str | None:
+    """What building _decode.so lacks here, None if nothing."""
+    import sysconfig
+    try:
+        import torch
+    except ImportError as e:
+        return f"torch does not import ({e})"
+    if torch.version.cuda is None:
+        return "torch is built without CUDA"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers are not installed"
+    if not (shutil.which("g++") or shutil.which("c++")):
+        return "no C++ compiler found"
+    return None
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:

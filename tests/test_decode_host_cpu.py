@@ -123,3 +123,20 @@ def test_entry_points_are_declared_in_one_place():
             text = f.read()
         assert '#include "decode_entry.h"' in text
         assert not re.search(r"^int awq_\w+_on\([^;{}]*\);$", text, re.M), name   # no declaration of its own
+
+
+@pytest.mark.parametrize("lacking", ["torch", "headers", "compiler"])
+def test_the_library_is_built_where_the_binding_cannot_be(monkeypatch, capsys, lacking):
+    import sys
+    import sysconfig
+
+    from post_quantization_column_b200 import build
+    build.build()   # nothing left to compile
+    if lacking == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    elif lacking == "headers":
+        monkeypatch.setattr(sysconfig, "get_paths", lambda: {"include": "/nowhere"})
+    else:
+        monkeypatch.setattr(build.shutil, "which", lambda name: None)
+    assert build.build() == build.LIB
+    assert "_decode.so is not built" in capsys.readouterr().err
