@@ -451,8 +451,9 @@ int awq_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, 
  *   out[b][h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q[b][h] . k_t - max)
  * with the key-value head h / (Hq / heads). q [n_seqs][Hq][D] (AWQ_DTYPE_F16 or _BF16, of the
  * cache's type if that has 16 bits; rows 16-byte aligned), out [n_seqs][Hq][D] contiguous of
- * q's type. Scores, maximum and sums are fp32; the weights p_t enter the product with v in 16
- * bits, and the sum that divides is of those. lengths[b] <= 0 gives zeros. A length beyond
+ * q's type. Scores, maximum and sums are fp32; the weights p_t enter the product with v as
+ * two 16-bit values, the rounded weight and its rounded rest (over an e4m3 cache as one fp16 value), and the
+ * sum that divides is of those. lengths[b] <= 0 gives zeros. A length beyond
  * max_pages * page_size, or a needed page outside the cache, makes that sequence's output NaN
  * and sets *status (device or pinned host memory, may be NULL, never cleared) to
  * AWQ_ERR_INVALID_ARG. `workspace`: at least

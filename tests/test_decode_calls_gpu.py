@@ -271,3 +271,46 @@ def test_a_first_call_may_be_a_captured_one():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     done = subprocess.run([sys.executable, "-c", _CAPTURED_FIRST.format(root=root)], capture_output=True, text=True, timeout=300)
     assert done.returncode == 0 and "captured first: ok" in done.stdout, done.stdout + done.stderr
+
+
+# ---- the attention's weights ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Dh,Hq,H", [(128, 8, 2), (128, 32, 2), (64, 12, 4), (256, 4, 4)])
+def test_attention_weights_keep_the_bits_of_fp32(dtype, Dh, Hq, H):
+    """Against 64 bits, with nothing allowed for a rounding of the weights to 16 bits. Keys and queries
+    are -1, 0 or 1 and the scale 1/8, so that every score is exact. With u = 2^-24 and h half a step
+    of the dtype at 1, a weight (as a factor) is off by 4 u |s| for the scale in base 2, twice for its
+    difference from the maximum, by 2^-21 for the exponential and by h^2 for the rest's rounding, together
+    E; in fp16 weights below 2^-14, of a sum of at least 2^7, are off by 2^-25 each. The fp32 sums
+    over n tokens add (n / 32 + 64) 2 u, and the output is rounded once."""
+    lens = [1, 17, 40, 63, 64, 65, 300, 1000, 0, 5000]
+    g = torch.Generator().manual_seed(Dh + Hq)
+    pages = sum(-(-n // 16) for n in lens)
+    signs = lambda *shape: torch.randint(-1, 2, shape, generator=g).to(dtype).cuda()  # noqa: E731
+    q, kc = signs(len(lens), Hq, Dh), signs(pages, 16, H, Dh)
+    vc = torch.randn(pages, 16, H, Dh, generator=g).to(dtype).cuda()
+    order, table, at = torch.randperm(pages, generator=g).to(torch.int32), torch.zeros(len(lens), 5000 // 16 + 1, dtype=torch.int32), 0
+    for b, n in enumerate(lens):
+        need = -(-n // 16)
+        table[b, :need] = order[at:at + need]
+        at += need
+    out = awq.paged_attention(q, kc, vc, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), 0.125)
+    u, h = 2.0 ** -24, torch.finfo(dtype).eps / 2
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert (out[b] == 0).all()
+            continue
+        ids = table[b, : -(-n // 16)].long().cuda()
+        k, v = (c[ids].reshape(-1, H, Dh)[:n].double().repeat_interleave(Hq // H, dim=1).transpose(0, 1) for c in (kc, vc))
+        s = 0.125 * (k @ q[b].double()[:, :, None])[..., 0]                     # (Hq, n)
+        p = torch.softmax(s, dim=1)
+        want = (p[:, None] @ v)[:, 0]
+        E = 8 * u * s.abs().amax(dim=1) + 4 * u * (s.amax(dim=1, keepdim=True) - s).amax(dim=1) + 2.0 ** -21 + h * h
+        off = (p[:, None] @ (v - want[:, None]).abs())[:, 0] * (E / (1 - E))[:, None]
+        off += (n / 32 + 64) * 2 * u * (p[:, None] @ v.abs())[:, 0]
+        if dtype == F16:
+            off += n * 2.0 ** -32 * (v - want[:, None]).abs().amax(dim=1)
+        off += torch.maximum(h * (want.abs() + off), torch.tensor(torch.finfo(dtype).smallest_normal * h, dtype=torch.float64, device="cuda"))
+        bad = ~((out[b].double() - want).abs() <= off)
+        assert not bad.any(), (n, int(bad.sum()), float(((out[b].double() - want).abs() / off).max()))
