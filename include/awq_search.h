@@ -381,7 +381,11 @@ int awq_w4a16_dequant(const int32_t* codes, const void* steps, const void* zeros
  * AWQ_DTYPE_F32, _F16 or _BF16; rows x_stride, r_stride and ro_stride apart. out [M][K]
  * contiguous holds one of these types, or AWQ_DTYPE_E4M3: out_scales[m] = max_k |y| / 448 (1
  * where that is zero) and out = e4m3(y / out_scales[m]); a row with a NaN or an infinity has
- * a NaN scale. 0 <= M < 2^31 (0 does nothing), 1 <= K <= 57344. Rows of aligned 16-byte
+ * a NaN scale. h weight and the sum of h^2 have to be within fp32's range: a row whose sum is beyond it
+ * (a root mean square above sqrt(3.4e38 / K), 2.9e17 at K = 4096) is divided by infinity and comes out as
+ * zeros, with scale 1; of values below 1e-19 the squares lose bits, which counts only for eps = 0,
+ * where values that are all below 2.6e-23 give infinities and a row of zeros 0 / 0, NaN with a NaN
+ * scale. 0 <= M < 2^31 (0 does nothing), 1 <= K <= 57344. Rows of aligned 16-byte
  * vectors (K % 8 == 0, K <= 16384) are the fastest, then rows of any other length from 64 to
  * 16384 that follow one another without a gap. */
 int awq_rms_norm(const void* X, int x_dtype, int64_t x_stride, const void* residual, int r_dtype,

@@ -737,8 +737,9 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residu
     bf16. The residual is replaced by the rounded h, in place or in ``residual_out``.
 
     Returns y (M, K) in ``out_dtype`` (fp16, bf16 or fp32), or for torch.float8_e4m3fn
-    ``(codes, scales)``: codes = e4m3(y / scales), one fp32 scale max|y| / 448 per row.
-    Asynchronous on `stream`."""
+    ``(codes, scales)``: codes = e4m3(y / scales), one fp32 scale max|y| / 448 per row. The sum of
+    h^2 is fp32: a row whose sum is beyond its range (root mean square above 2.9e17 at K = 4096) gives
+    zeros. Asynchronous on `stream`."""
     args = (X, weight, eps, residual, residual_out, out_dtype)
     call = (_decode_module or _load_decode()).rms_norm
     out = call(*args) if stream is None else _on_stream(stream, call, args)

@@ -10,7 +10,8 @@
 // keeps order, so max|y| = fl(max|h w| / sqrt(...)): one reduction of (sum h^2, max|h w|)
 // per row serves both forms. The maximum is taken of the bit patterns of |h w|, which
 // order as the values do and put NaN above everything: a row that holds a NaN or an
-// infinity has a NaN scale.
+// infinity has a NaN scale. The squares are not scaled before they are added: a sum beyond fp32
+// divides its row by infinity, and with eps = 0 one that underflows divides it by zero.
 //
 // What bounds it: the rows' bytes, each read and written once (x, r, r' and y; 1 GB for 16384 x
 // 8192 in bf16 with a residual). A row stays in registers between its statistic and its output,

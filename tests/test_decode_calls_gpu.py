@@ -110,6 +110,34 @@ def test_long_rows_that_start_between_vectors(offset):
     assert torch.equal(rbase, before)   # nothing beside the rows was written
 
 
+@pytest.mark.parametrize("K", [512, 515, 4096, 20001])
+def test_norm_at_the_ends_of_its_range(K):
+    """What the header says of sums beyond fp32 and of eps = 0; within the range, the formula."""
+    w = _randn(K, seed=1)
+    X = _randn(5, K, seed=2)
+    X[1] *= 1e16                      # K 1e32 < 3.4e38
+    X[2] *= 1e20                      # its sum is beyond fp32
+    X[3] = 0.0
+    X[4] *= 1e-15
+    for M in (5, 300):
+        rows = X.repeat(M // 5, 1)
+        fine = [m for m in range(M) if m % 5 != 2]
+        out = awq.rms_norm(rows, w, out_dtype=F32)
+        _check_norm(rows[fine], w, out[fine])
+        assert (out[2] == 0).all()
+        codes, scales = awq.rms_norm(rows, w, out_dtype=E4M3)
+        _check_norm(rows[fine], w, (codes[fine], scales[fine]))
+        assert (codes[2].float() == 0).all() and scales[2] == 1.0
+        fine = [m for m in range(M) if m % 5 not in (2, 3)]
+        out = awq.rms_norm(rows, w, 0.0, out_dtype=F32)
+        _check_norm(rows[fine], w, out[fine], eps=0.0)
+        assert torch.isnan(out[3]).all()
+        codes, scales = awq.rms_norm(rows, w, 0.0, out_dtype=E4M3)
+        assert torch.isnan(scales[3]) and torch.isnan(codes[3].float()).all()
+    tiny = torch.full((2, K), 1e-25, device="cuda")
+    assert torch.isinf(awq.rms_norm(tiny, torch.ones(K, device="cuda"), 0.0, out_dtype=F32)).all()
+
+
 # ---- the binding -----------------------------------------------------------------------------------
 
 def _decode_inputs():
