@@ -48,7 +48,7 @@ Extent extent(const PagedCache& c, const void* p) {
 }
 bool meet(const Extent& a, const Extent& b) { return a.from < b.to && b.from < a.to; }
 
-constexpr int kAsk = -1;  // the device of the call is asked of its pointers
+constexpr int kAsk = -1;  // the device of the call is asked of its pointers (else the binding calls, with outputs of its own)
 
 // Makes the device of the call current: the caller's, which owns all its pointers (the Python
 // binding knows its tensors' device), or that of `first`, where every pointer must lie. A kernel that
@@ -167,7 +167,7 @@ int awq_rms_norm_on(int device, const void* X, int x_dtype, int64_t x_stride, co
       (residual && (ranges_meet(residual, r_stride * rb, K * rb, out, K * ob, K * ob, M) ||
                     ranges_meet(residual_out, ro_stride * rb, K * rb, out, K * ob, K * ob, M))))
     return decode_error(AWQ_ERR_INVALID_ARG, "out must not overlap another argument");
-  if (out_dtype == kTypeE4m3) {
+  if (out_dtype == kTypeE4m3 && device == kAsk) {
     const Extent to = extent(out_scales, M, 4, 1, 0, 4);
     if (meet(to, extent(X, M, x_stride * xb, 1, 0, K * xb)) || meet(to, extent(weight, 1, 0, 1, 0, K * wb)) ||
         meet(to, extent(out, M, K, 1, 0, K)) ||
@@ -278,7 +278,7 @@ int awq_kv_append_on(int device, const void* q, int64_t q_token_stride, int64_t 
   if (!rows_apart(a.c)) return decode_error(AWQ_ERR_INVALID_ARG, "rows of a cache that is written must not overlap");
   if (!aligned(positions, 4) || !aligned(seqs, 4) || !aligned(freqs, 8) || !aligned(status, 4))
     return decode_error(AWQ_ERR_INVALID_ARG, "positions, seqs, freqs or status is misaligned");
-  if (Hq > 0) {  // every unit of q is read and written by one thread, so that q_out may be q
+  if (Hq > 0 && device == kAsk) {  // every unit of q is read and written by one thread, so that q_out may be q
     const int64_t D = a.c.head_dim, b = type_bytes(in_dtype);
     const Extent to = extent(q_out, T, Hq * D * 2, Hq, D * 2, D * 2);
     const bool same = q_out == q && in_dtype == q_dtype && (T == 1 || q_token_stride == Hq * D) && (Hq == 1 || q_head_stride == D);
@@ -358,7 +358,7 @@ int awq_paged_attention_on(int device, const void* q, int64_t q_seq_stride, int6
   if (!aligned(lengths, 4) || !aligned(status, 4)) return decode_error(AWQ_ERR_INVALID_ARG, "lengths or status is misaligned");
   if (workspace_bytes < awq_paged_attention_workspace(Hq, a.c.heads, a.c.head_dim, a.c.type))
     return decode_error(AWQ_ERR_INVALID_ARG, "the work space is smaller than awq_paged_attention_workspace says");
-  {  // a segment's queries are read before any of its outputs are written, so that out may be q
+  if (device == kAsk) {  // a segment's queries are read before any of its outputs are written, so that out may be q
     const int64_t B = a.c.seqs, D = a.c.head_dim;
     const Extent to = extent(out, B, Hq * D * 2, Hq, D * 2, D * 2), from = extent(q, B, q_seq_stride * 2, Hq, q_head_stride * 2, D * 2),
                  ws = extent(workspace, 1, 0, 1, 0, workspace_bytes), ck = extent(a.c, a.c.k), cv = extent(a.c, a.c.v);

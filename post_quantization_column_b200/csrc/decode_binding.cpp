@@ -61,6 +61,7 @@ Tensor maybe(PyObject* o, const char* what) { return o == Py_None ? Tensor() : t
 void on_device(const Tensor& t, const at::Device& device) {
   if (!t.defined()) return;
   value_check(t.device() == device, "every tensor must be on the device of the first");
+  if (t.unsafeGetTensorImpl()->autograd_meta() == nullptr) return;  // as most
   value_check(!(t.requires_grad() && at::GradMode::is_enabled()),
               "the decode-step operators have no backward pass: call them under torch.no_grad()");
   value_check(!(c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined()),
