@@ -14,7 +14,7 @@
 // per block of a token, while its values are on the way; a thread turns 16 values of a head. In
 // a captured graph 4096 tokens of 32 + 2 x 32 bf16 heads take 35 us, 5.7 TB/s (address and
 // conversion instructions keep the issue slots half busy), 2047 tokens of 64 + 2 x 8 fp32 heads
-// 20 us, 6.3 TB/s, one token 2.0 us. A persistent form that loads the next token's values early
+// 20 us, 6.3 TB/s, one token 1.8 us. A persistent form that loads the next token's values early
 // took 50 us for the former: its registers halve the blocks an SM holds.
 #include "decode_kernels.h"
 

@@ -3,22 +3,22 @@
 //   o_h = (sum_t p_t v_t) / (sum_t p_t),  p_t = 2^(s_t - m),  s_t = scale log2(e) q_h . k_t
 //
 // over the sequence's first `length` cached tokens, with the running maximum m of the scores
-// met so far (the sums are rescaled when it grows), so the cache is read once. Every group
-// of Hq / Hkv query heads shares its key-value head's bytes: they are read once for the group.
+// met so far (the sums are rescaled when it grows), so the cache is read once for up to 8 query heads
+// of a key-value head (16 where heads have 64 or 128 dims), which share its bytes. More query
+// heads than that make another pass over them.
 //
 // What bounds it: the cache's bytes (each of 2 D values per token and key-value head is used in
 // Hq / Hkv multiply-adds), so the kernel is a stream.
 //
-// Work. The unit is 32 KB of the cache: 64 tokens of one (sequence, key-value head) at D = 128
-// in 16 bits, more where rows are shorter. All units of the batch, sequence-major, are dealt to
-// a grid of as many CTAs as fit the SMs, in equal contiguous runs, whatever the lengths are; a CTA
-// finds its run from the lengths on the device. A (sequence, head) that lies within one run is
+// Work. The unit is 64 tokens of one (sequence, key-value head), more where rows are shorter than 256
+// bytes: 32 KB of the cache, or 64 KB with 16-bit heads of 256. All units of the batch, sequence-major,
+// are dealt to a grid of as many CTAs as fit the SMs, in equal contiguous runs; a CTA finds its run from the lengths on the device. A (sequence, head) that lies within one run is
 // finished there; one that crosses runs leaves a partial (o, m, l) per run, and a second
 // kernel adds them in run order (fixed order: equal inputs give equal bits). That join costs
 // 3 to 5 us, so where the longest sequence has at most kWhole units runs begin and end with
 // segments instead (55 sequences of 128 tokens, 8 heads: 8.7 us against 12.4 cut and joined).
 //
-// Tile. A warp takes 8 KB (16 tokens at D = 128 in 16 bits) of a unit with its own running
+// Tile. A warp takes a quarter of a unit (8 KB: 16 tokens at D = 128 in 16 bits) with its own running
 // maximum; the four warps meet once per (sequence, head). Tokens are the rows of both products,
 // so a group of up to 8 heads fills the 8 columns of an m16n8k16 MMA and none of the 16 rows is
 // padding:
@@ -32,13 +32,14 @@
 // cp.async stages took twice the time: eight warps' chains of shared-memory reads, shuffles
 // and products were longer than the loads; bulk copies of 128-byte rows stop at 3.9 TB/s.)
 // The MMAs are mma.sync: tcgen05 wants 64 rows or more of a tile in shared memory, and at one
-// token per sequence the tensor pipe is 10 % busy here.
+// token per sequence the tensor pipe is 15 % busy here.
 //
 // Measured (B200, device time in a captured graph; the copy rate is 6.55 TB/s): 16 x 4096 tokens
-// of 32 fp16 heads 163 us, 6.6 TB/s; 67 ragged sequences up to 8192, 8 bf16 heads shared by 64,
-// 189 us, 6.4 TB/s; one sequence of 131072 tokens 88 us, 6.1 TB/s; 96 ragged sequences up to
-// 4099 on an e4m3 cache 96 us, 4.6 TB/s (bound by the latency of a tile's chain: 131 of its 560
-// instructions unpack e4m3; 6.7 TB/s at the margin of longer sequences); one of 33 tokens 4.9 us.
+// of 32 fp16 heads 164 us, 6.6 TB/s; 67 ragged sequences up to 8192, 8 bf16 heads shared by 64,
+// 189 us, 6.4 TB/s; one sequence of 131072 tokens 89 us, 6.1 TB/s; 96 ragged sequences up to
+// 4099 on an e4m3 cache 96 us, 4.6 TB/s (bound by the latency of a tile's chain: 128 conversions and 32
+// byte shuffles of its 647 instructions unpack e4m3; 6.7 TB/s at the margin of longer sequences); one of
+// 33 tokens 4.7 us.
 #include "decode_kernels.h"
 
 #include <algorithm>
@@ -806,7 +807,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(PagedAttn
 }
 
 // Blocks of 8 query heads that share a pass over the cache: two where a group has more than 8 and
-// the registers hold both. Larger groups read the cache again, from L2 for the most part.
+// the registers hold both (64 ragged sequences up to 8192, 4 bf16 heads of 128: 117 us for 64 query heads, 100
+// for 32, whose pass of one block runs three CTAs an SM; the floor is 92). Larger groups read the
+// cache again, from DRAM in long sequences, since a segment's passes follow one another: 211 us for
+// 128 query heads there, and 190 for 64 on 4 heads of 256 (32 sequences) where 16 on 4 take 106.
 int head_blocks(int Hq, int Hkv, int D) { return Hq / Hkv > 8 && D <= 128 ? 2 : 1; }
 
 template <int D, int TYPE, int NB>
