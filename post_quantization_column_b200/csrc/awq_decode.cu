@@ -48,7 +48,8 @@ Extent extent(const PagedCache& c, const void* p) {
 }
 bool meet(const Extent& a, const Extent& b) { return a.from < b.to && b.from < a.to; }
 
-constexpr int kAsk = -1;  // the device of the call is asked of its pointers (else the binding calls, with outputs of its own)
+// The device of the call is asked of its pointers; else the binding calls, with outputs of its own.
+constexpr int kAsk = -1;
 
 // Makes the device of the call current: the caller's, which owns all its pointers (the Python
 // binding knows its tensors' device), or that of `first`, where every pointer must lie. A kernel that
@@ -356,12 +357,13 @@ int awq_paged_attention_on(int device, const void* q, int64_t q_seq_stride, int6
     return decode_error(AWQ_ERR_INVALID_ARG, "q, out and the work space must be 16-byte aligned");
   if (q_seq_stride < 0 || q_head_stride < 0) return decode_error(AWQ_ERR_INVALID_ARG, "strides must not be negative");
   if (!aligned(lengths, 4) || !aligned(status, 4)) return decode_error(AWQ_ERR_INVALID_ARG, "lengths or status is misaligned");
-  if (workspace_bytes < awq_paged_attention_workspace(Hq, a.c.heads, a.c.head_dim, a.c.type))
+  const int64_t used = awq_paged_attention_workspace(Hq, a.c.heads, a.c.head_dim, a.c.type);  // of the work space, which may be larger
+  if (workspace_bytes < used)
     return decode_error(AWQ_ERR_INVALID_ARG, "the work space is smaller than awq_paged_attention_workspace says");
   if (device == kAsk) {  // a segment's queries are read before any of its outputs are written, so that out may be q
     const int64_t B = a.c.seqs, D = a.c.head_dim;
     const Extent to = extent(out, B, Hq * D * 2, Hq, D * 2, D * 2), from = extent(q, B, q_seq_stride * 2, Hq, q_head_stride * 2, D * 2),
-                 ws = extent(workspace, 1, 0, 1, 0, workspace_bytes), ck = extent(a.c, a.c.k), cv = extent(a.c, a.c.v);
+                 ws = extent(workspace, 1, 0, 1, 0, used), ck = extent(a.c, a.c.k), cv = extent(a.c, a.c.v);
     const bool same = out == q && (B == 1 || q_seq_stride == Hq * D) && (Hq == 1 || q_head_stride == D);
     if ((!same && meet(to, from)) || meet(to, ws) || meet(to, ck) || meet(to, cv) || meet(ws, from) || meet(ws, ck) || meet(ws, cv))
       return decode_error(AWQ_ERR_INVALID_ARG, "out may be q itself; it and the work space overlap nothing else");

@@ -65,7 +65,7 @@ def test_outputs_that_overlap_other_arguments_are_refused():
             (lambda **kw: _attention(cache=_cache(num_pages=1, seqs=2, k=kb, v=vb), **kw),
              (dict(out=P + 16384 + 512), dict(out=kb), dict(out=vb + 8176), dict(ws=P + 16384 + 16), dict(ws=P + 24576 - 32), dict(ws=kb - 64),
               dict(out=P + 16384, qs=1024), dict(out=P + 16384 - 2032)),
-             (dict(), dict(out=P + 16384), dict(out=P + 16384 + 2048))),
+             (dict(), dict(out=P + 16384), dict(out=P + 16384 + 2048), dict(ws=P + (1 << 21), out=P + (1 << 29)))),   # in a larger buffer
             (_norm,
              (dict(sc=P), dict(sc=P + 2044), dict(sc=P + 8192 + 508), dict(sc=P + 16384 + 508), dict(r=P + 32768, ro=P + 32768, sc=P + 32768 + 64)),
              (dict(), dict(sc=P + 2048), dict(sc=P + 16384 + 512), dict(ot=2, sc=P)))):
